@@ -1,0 +1,218 @@
+// Residual update with the norms around it: gam_residual_norm.
+//
+//   x' = x + alpha * layer_scale * gate_act(gate) * post_norm(y),  u = pre_norm(x')
+//
+// One pass: a group of G threads (a warp, or a CTA for wide rows) holds a row of
+// y and x in registers, so each is read once; statistics are two-pass in fp32
+// (mean, then the centred squares) over those registers.
+#include "stream_ops.cuh"
+
+namespace gam {
+namespace ops {
+namespace {
+
+// Sum over the G threads of a row: a warp by shuffles, a CTA through shared
+// memory (red holds two alternating sets of 32 partial sums, so one barrier per
+// sum is enough).
+template <bool WARP>
+__device__ __forceinline__ float row_sum(float v, float (*red)[32], int& turn) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  if constexpr (WARP) return v;
+  const int lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+  float* r = red[turn];
+  turn ^= 1;
+  if (lane == 0) r[threadIdx.x >> 5] = v;
+  __syncthreads();
+  v = lane < warps ? r[lane] : 0.f;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
+template <int V>
+__device__ __forceinline__ void load_param(const float* p, int c, float fill, float (&out)[V]) {
+#pragma unroll
+  for (int i = 0; i < V; ++i) out[i] = p ? __ldg(p + c + i) : fill;
+}
+
+// v <- norm(v) over the row; thread tid of G holds columns (j G + tid) V + i
+template <bool WARP, int V, int NV>
+__device__ __forceinline__ void norm_row(float (&v)[NV][V], int kind, const float* w, const float* b, float eps, int d,
+                                         int tid, int G, float (*red)[32], int& turn) {
+  if (kind == GAM_NORM_LAYER) {
+    float s = 0.f;
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+#pragma unroll
+      for (int i = 0; i < V; ++i) s += v[j][i];
+    const float mean = row_sum<WARP>(s, red, turn) / d;
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+#pragma unroll
+      for (int i = 0; i < V; ++i) v[j][i] = (j * G + tid) * V < d ? v[j][i] - mean : 0.f;
+  }
+  float q = 0.f;
+#pragma unroll
+  for (int j = 0; j < NV; ++j)
+#pragma unroll
+    for (int i = 0; i < V; ++i) q = fmaf(v[j][i], v[j][i], q);
+  const float r = rsqrtf(row_sum<WARP>(q, red, turn) / d + eps);
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    const int c = (j * G + tid) * V;
+    if (c < d) {
+      float ww[V], bb[V];
+      load_param<V>(w, c, 1.f, ww);
+      load_param<V>(kind == GAM_NORM_LAYER ? b : nullptr, c, 0.f, bb);
+#pragma unroll
+      for (int i = 0; i < V; ++i) v[j][i] = fmaf(v[j][i] * r, ww[i], bb[i]);
+    }
+  }
+}
+
+template <typename TX, typename TY, bool WARP, int V, int NV>
+__global__ void __launch_bounds__(WARP ? 128 : V == 8 ? 512 : 1024) residual_norm_kernel(const gam_residual_norm_args p, int64_t per_gate) {
+  __shared__ float red[2][32];
+  const int G = WARP ? 32 : blockDim.x;
+  const int tid = WARP ? threadIdx.x & 31 : threadIdx.x;
+  const int64_t row = WARP ? (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5) : (int64_t)blockIdx.x;
+  if (row >= p.rows) return;
+  const int d = p.d;
+  int turn = 0;
+  float x[NV][V], y[NV][V];
+  const TX* xr = (const TX*)p.x + row * p.x_stride;
+  const TY* yr = (const TY*)p.y + row * p.y_stride;
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    const int c = (j * G + tid) * V;
+    if (c < d) {
+      const Vec<TX, V> a = *reinterpret_cast<const Vec<TX, V>*>(xr + c);
+      const Vec<TY, V> b = *reinterpret_cast<const Vec<TY, V>*>(yr + c);
+#pragma unroll
+      for (int i = 0; i < V; ++i) x[j][i] = to_f(a.v[i]), y[j][i] = to_f(b.v[i]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < V; ++i) x[j][i] = y[j][i] = 0.f;
+    }
+  }
+  if (p.post_norm) norm_row<WARP, V, NV>(y, p.post_norm, p.post_weight, p.post_bias, p.eps, d, tid, G, red, turn);
+  const TY* gr = p.gate ? (const TY*)p.gate + row / per_gate * p.gate_stride : nullptr;
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    const int c = (j * G + tid) * V;
+    if (c < d) {
+      if (gr) {
+        const Vec<TY, V> g = *reinterpret_cast<const Vec<TY, V>*>(gr + c);
+#pragma unroll
+        for (int i = 0; i < V; ++i) y[j][i] *= activate(to_f(g.v[i]), p.gate_act);
+      }
+      float ls[V];
+      load_param<V>(p.layer_scale, c, 1.f, ls);
+#pragma unroll
+      for (int i = 0; i < V; ++i) x[j][i] = fmaf(p.alpha * ls[i], y[j][i], x[j][i]);
+      if (p.x_out) {
+        Vec<TX, V> o;
+#pragma unroll
+        for (int i = 0; i < V; ++i) o.v[i] = from_f<TX>(x[j][i]);
+        *reinterpret_cast<Vec<TX, V>*>((TX*)p.x_out + row * p.x_out_stride + c) = o;
+      }
+    }
+  }
+  if (!p.u) return;
+  if (p.pre_norm) norm_row<WARP, V, NV>(x, p.pre_norm, p.pre_weight, p.pre_bias, p.eps, d, tid, G, red, turn);
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    const int c = (j * G + tid) * V;
+    if (c < d) {
+      Vec<TY, V> o;
+#pragma unroll
+      for (int i = 0; i < V; ++i) o.v[i] = from_f<TY>(x[j][i]);
+      *reinterpret_cast<Vec<TY, V>*>((TY*)p.u + row * p.u_stride + c) = o;
+    }
+  }
+}
+
+template <typename TX, typename TY, int V>
+gam_status launch_v(const gam_residual_norm_args& p, int64_t per_gate, cudaStream_t s) {
+  const int vecs = (p.d + V - 1) / V;
+  if (vecs <= 128) {  // a warp holds a row: up to 4 accesses per lane
+    const int64_t grid = (p.rows + 3) / 4;
+    if (grid > INT32_MAX) return op_fail(GAM_ERR_CAPACITY, "too many rows for one call");
+    if (vecs <= 32) residual_norm_kernel<TX, TY, true, V, 1><<<(unsigned)grid, 128, 0, s>>>(p, per_gate);
+    else if (vecs <= 64) residual_norm_kernel<TX, TY, true, V, 2><<<(unsigned)grid, 128, 0, s>>>(p, per_gate);
+    else residual_norm_kernel<TX, TY, true, V, 4><<<(unsigned)grid, 128, 0, s>>>(p, per_gate);
+    return launch_status(cudaGetLastError());
+  }
+  if (p.rows > INT32_MAX) return op_fail(GAM_ERR_CAPACITY, "too many rows for one call");
+  const unsigned grid = (unsigned)p.rows;
+  auto threads = [&](int nv) { return ((vecs + nv - 1) / nv + 31) / 32 * 32; };
+  if (vecs <= 1024) residual_norm_kernel<TX, TY, false, V, 2><<<grid, threads(2), 0, s>>>(p, per_gate);
+  else if (vecs <= 4096) residual_norm_kernel<TX, TY, false, V, 4><<<grid, threads(4), 0, s>>>(p, per_gate);
+  else if constexpr (V == 1) residual_norm_kernel<TX, TY, false, V, 16><<<grid, threads(16), 0, s>>>(p, per_gate);
+  return launch_status(cudaGetLastError());
+}
+
+template <typename TX, typename TY>
+gam_status launch(const gam_residual_norm_args& p, int64_t per_gate, cudaStream_t s) {
+  constexpr int V = 16 / sizeof(TY);
+  const bool wide = p.d % V == 0 && aligned(p.x, 16) && aligned(p.y, 16) && aligned(p.gate, 16) &&
+                    aligned(p.x_out, 16) && aligned(p.u, 16) && p.x_stride % V == 0 && p.y_stride % V == 0 &&
+                    p.gate_stride % V == 0 && p.x_out_stride % V == 0 && p.u_stride % V == 0;
+  return wide ? launch_v<TX, TY, V>(p, per_gate, s) : launch_v<TX, TY, 1>(p, per_gate, s);
+}
+
+bool norm_kind(int k) { return k == GAM_NORM_NONE || k == GAM_NORM_LAYER || k == GAM_NORM_RMS; }
+
+}  // namespace
+}  // namespace ops
+}  // namespace gam
+
+using namespace gam::ops;
+
+extern "C" gam_status gam_residual_norm(const gam_residual_norm_args* args, void* stream) {
+  return guarded([&] {
+    if (!args) return op_fail(GAM_ERR_INVALID_ARG, "null args");
+    gam_residual_norm_args p = *args;
+    if (!is_float_dtype(p.dtype)) return op_fail(GAM_ERR_INVALID_ARG, "dtype must be f32, f16 or bf16");
+    if (p.x_dtype != p.dtype && p.x_dtype != GAM_DTYPE_F32)
+      return op_fail(GAM_ERR_INVALID_ARG, "x_dtype must be dtype or f32");
+    if (!norm_kind(p.post_norm) || !norm_kind(p.pre_norm)) return op_fail(GAM_ERR_INVALID_ARG, "unknown norm");
+    if (p.gate_act < GAM_ACT_NONE || p.gate_act > GAM_ACT_TANH) return op_fail(GAM_ERR_INVALID_ARG, "unknown gate_act");
+    if (p.rows < 0 || p.d < 1) return op_fail(GAM_ERR_INVALID_ARG, "rows >= 0 and d >= 1");
+    if (p.d > 16384) return op_fail(GAM_ERR_CAPACITY, "d above 16384");
+    if ((p.post_norm || p.pre_norm) && !(p.eps >= 0.f)) return op_fail(GAM_ERR_INVALID_ARG, "eps must be >= 0");
+    if (p.rows == 0) return GAM_OK;
+    if (!p.x || !p.y || (!p.x_out && !p.u)) return op_fail(GAM_ERR_INVALID_ARG, "null pointer");
+    if (!p.gate) p.gate_rows = 1, p.gate_stride = 0;
+    if (p.gate_rows < 1 || p.rows % p.gate_rows) return op_fail(GAM_ERR_SHAPE, "rows must be a multiple of gate_rows");
+    if (!p.x_out) p.x_out_stride = p.x_stride;
+    if (!p.u) p.u_stride = p.y_stride;
+    if (p.rows == 1) p.x_stride = p.y_stride = p.x_out_stride = p.u_stride = p.gate_stride = p.d;
+    if (p.rows > 1 && (p.x_stride < p.d || p.y_stride < p.d || p.x_out_stride < p.d || p.u_stride < p.d))
+      return op_fail(GAM_ERR_SHAPE, "rows must be at least d apart");
+    if (p.gate && p.gate_rows > 1 && p.gate_stride < p.d) return op_fail(GAM_ERR_SHAPE, "gate rows must be at least d apart");
+    const int es = dtype_size(p.dtype), xs = dtype_size(p.x_dtype);
+    if (!aligned(p.x, xs) || !aligned(p.x_out, xs) || !aligned(p.y, es) || !aligned(p.u, es) || !aligned(p.gate, es) ||
+        !aligned(p.layer_scale, 4) || !aligned(p.post_weight, 4) || !aligned(p.post_bias, 4) ||
+        !aligned(p.pre_weight, 4) || !aligned(p.pre_bias, 4))
+      return op_fail(GAM_ERR_INVALID_ARG, "a buffer is not aligned to its element type");
+    if ((p.x_out == p.x && p.x_out_stride != p.x_stride) || (p.u == p.y && p.u_stride != p.y_stride))
+      return op_fail(GAM_ERR_INVALID_ARG, "a call in place keeps the row stride");
+    if (p.u && (p.u == p.x || p.u == p.gate || p.u == p.x_out))
+      return op_fail(GAM_ERR_INVALID_ARG, "u may share a buffer with y only");
+    if (p.x_out && (p.x_out == p.y || p.x_out == p.gate))
+      return op_fail(GAM_ERR_INVALID_ARG, "x_out may share a buffer with x only");
+    int sms = 0;
+    if (gam_status st = check_device(&sms)) return st;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const int64_t per_gate = p.rows / p.gate_rows;
+    if (p.x_dtype == GAM_DTYPE_F32) {
+      if (p.dtype == GAM_DTYPE_F32) return launch<float, float>(p, per_gate, s);
+      if (p.dtype == GAM_DTYPE_F16) return launch<float, __half>(p, per_gate, s);
+      return launch<float, bf16>(p, per_gate, s);
+    }
+    if (p.dtype == GAM_DTYPE_F16) return launch<__half, __half>(p, per_gate, s);
+    return launch<bf16, bf16>(p, per_gate, s);
+  });
+}

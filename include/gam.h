@@ -72,8 +72,8 @@ typedef enum {
  * dequantised to fp16 inside the tensor-core GEMM's mainloop. */
 enum { GAM_FP32 = 0, GAM_FP16 = 1, GAM_INT8_G64 = 2, GAM_INT6_G64 = 3, GAM_INT4_G64 = 4 };
 
-/* gam_tensor.dtype */
-enum { GAM_DTYPE_F32 = 0, GAM_DTYPE_F16 = 1, GAM_DTYPE_I8 = 2 };
+/* gam_tensor.dtype; GAM_DTYPE_BF16 is for the streaming-block operators only. */
+enum { GAM_DTYPE_F32 = 0, GAM_DTYPE_F16 = 1, GAM_DTYPE_I8 = 2, GAM_DTYPE_BF16 = 3 };
 
 /* Stage ids of gam_encode_stage (the residual stream after each step). */
 enum {
@@ -123,7 +123,8 @@ const char* gam_status_string(gam_status status);
 
 /* Text of the last error seen by this context ("" if none).  A NULL ctx gives
  * the last error on this thread of the calls that take no context
- * (gam_create, gam_plan_lengths, gam_ctc_collapse_noalloc). */
+ * (gam_create, gam_plan_lengths, gam_ctc_collapse_noalloc and the
+ * streaming-block operators). */
 const char* gam_last_error(const gam_ctx* ctx);
 
 /* Lengths of the frontend and subsampling ("GigaAM v3 MLX", "Frontend
@@ -334,6 +335,149 @@ gam_status gam_stream_reset(gam_stream* st);
  * window, and text at its start can change from step to step. */
 gam_status gam_stream_push(gam_stream* st, const float* samples_host, int64_t n, int32_t* tokens_host,
                            int max_tokens, int32_t* count_out, int64_t* window_start_out, void* stream);
+
+/* ---- streaming-block operators ---- */
+
+/* The pages' model re-recognises a growing window at every step ("GigaAM on
+ * MLX: the transcripts matched, but the model was broken", "Streaming").  The
+ * four operators below are the parts of a block that carries a state of fixed
+ * size instead and so takes each frame once: a linear layer on the library's
+ * INT4-g64 weights for a few rows, a causal depthwise convolution, a selective
+ * state-space scan, and the residual update with the norms around it (the
+ * macaron half-weight residual and LayerNorm chain, with a norm, a gate and a
+ * scale on the branch).  The pages have no counterpart; each operator's
+ * formula, given here, is its definition.
+ *
+ * They take no context, keep no state of their own between calls and allocate
+ * nothing: every buffer is the caller's.  They run on the current device, which
+ * must own the buffers, and on `stream`; they neither synchronise nor read
+ * device memory on the host, so they can be captured into a CUDA graph, and
+ * calls on several streams or threads do not disturb one another as long as
+ * their outputs are distinct.  Errors go to gam_last_error(NULL).
+ *
+ * `dtype` (GAM_DTYPE_F32, _F16 or _BF16) is the type of the activations; sums,
+ * statistics and scan states are fp32 and an output is rounded once.  Strides
+ * are in elements; the last dimension is contiguous.  Pointers need the
+ * alignment of their element type only (16-byte aligned rows are faster),
+ * except packed weights, which need 16 bytes.  Outputs must not overlap inputs
+ * or one another unless a call says so.  A call with no rows or no sequences
+ * does nothing and succeeds. */
+
+/* Activation of an operator's result or gate: v, v sigmoid(v), sigmoid(v) or
+ * tanh(v). */
+enum { GAM_ACT_NONE = 0, GAM_ACT_SWISH = 1, GAM_ACT_SIGMOID = 2, GAM_ACT_TANH = 3 };
+
+/* Largest number of rows of one gam_quant_linear call. */
+#define GAM_QUANT_LINEAR_MAX_ROWS 64
+
+/* INT4-g64 weights (GAM_INT4_G64, "<name>.weight_q") in the packed form that
+ * gam_quant_linear reads.  Host only: q_host int8 [n, k], every value in
+ * [-7, 7] (else GAM_ERR_WEIGHTS), k a multiple of 64; packed_host receives
+ * n * k / 2 bytes.  Row o holds its k weights in order, 8 to a little-endian
+ * 32-bit word: weight v_j of the word is stored as v_j + 8, v_2i in bits
+ * 4 i .. 4 i + 3 and v_2i+1 in bits 16 + 4 i .. 16 + 4 i + 3. */
+gam_status gam_quant_linear_pack(const int8_t* q_host, int64_t n, int64_t k, uint8_t* packed_host);
+
+/* Linear layer with INT4-g64 weights for a few rows:
+ *   y[m, o] = act(bias[o] + sum_g scale[o, g] sum_{j in group g} q[o, j] x[m, j])
+ * x_dev: device dtype [rows, k], rows ldx apart (ldx >= k when rows > 1);
+ * packed_dev: device, 16-byte aligned, as gam_quant_linear_pack lays it out;
+ * scale_dev: device f16 [n, k/64]; bias_dev (optional): device f32 [n];
+ * y_dev: device dtype [rows, n], rows ldy apart (ldy >= n).  rows 0 ..
+ * GAM_QUANT_LINEAR_MAX_ROWS (GAM_ERR_CAPACITY above), n >= 1, k a multiple of
+ * 64 (GAM_ERR_SHAPE); act GAM_ACT_NONE or GAM_ACT_SWISH.  Unlike the encoder's
+ * INT4 mode, which rounds q scale to fp16, neither the weights nor (in fp32) x are
+ * rounded: products and sums are fp32.  What a row holds, infinities and NaN
+ * included, does not reach other rows, and equal calls give equal bits. */
+gam_status gam_quant_linear(const void* x_dev, int dtype, int64_t ldx, const uint8_t* packed_dev,
+                            const void* scale_dev, const float* bias_dev, int act, int rows, int n, int k,
+                            void* y_dev, int64_t ldy, void* stream);
+
+/* Causal depthwise convolution over time, for prompts and for single frames:
+ *   y[b, t, c] = act(bias[c] + sum_{j < taps} w[c, j] v[b, t + j, c])
+ * where v is the state's taps - 1 rows followed by x's rows.  x_dev: device
+ * dtype [batch, t_max, d], sequences x_batch_stride and rows x_row_stride
+ * apart; w_dev: device f32 [d, taps] (PyTorch's depthwise [d, 1, taps]), taps
+ * 2 .. 8; bias_dev (optional): device f32 [d]; act GAM_ACT_NONE or
+ * GAM_ACT_SWISH.  lengths_dev (optional): device i32 [batch], valid frames of
+ * each sequence, clamped to [0, t_max]; frames beyond are written as zeros and
+ * never read.  state_in_dev (optional, else zeros): device dtype [batch,
+ * taps - 1, d], the inputs before frame 0, oldest first; state_out_dev
+ * (optional): the same after the last valid frame, and may be state_in_dev.
+ * y_dev: device dtype [batch, t_max, d] with strides y_batch_stride,
+ * y_row_stride.  t_max >= 0: with no frames the state is handed on. */
+gam_status gam_short_conv(const void* x_dev, int dtype, int64_t x_batch_stride, int64_t x_row_stride,
+                          const float* w_dev, const float* bias_dev, int taps, int act, int batch, int t_max, int d,
+                          const int32_t* lengths_dev, const void* state_in_dev, void* state_out_dev, void* y_dev,
+                          int64_t y_batch_stride, int64_t y_row_stride, void* stream);
+
+/* Arguments of gam_selective_scan.  Strides in elements. */
+typedef struct {
+  const void* x;          /* dtype [batch, t_max, d]                               */
+  const void* dt;         /* dtype [batch, t_max, d]: step sizes before the bias    */
+  const float* a;         /* f32 [d, n]: decay rates                               */
+  const void* b;          /* dtype [batch, t_max, n]                               */
+  const void* c;          /* dtype [batch, t_max, n]                               */
+  const float* d_skip;    /* f32 [d], optional (0)                                 */
+  const void* z;          /* dtype [batch, t_max, d], optional (no gate)           */
+  const float* dt_bias;   /* f32 [d], optional (0)                                 */
+  const int32_t* lengths; /* i32 [batch], optional (t_max), clamped to [0, t_max]  */
+  const float* state_in;  /* f32 [batch, d, n], optional (0)                       */
+  float* state_out;       /* f32 [batch, d, n], optional; may be state_in          */
+  void* y;                /* dtype [batch, t_max, d]                               */
+  int64_t x_batch_stride, x_row_stride;
+  int64_t dt_batch_stride, dt_row_stride;
+  int64_t b_batch_stride, b_row_stride;
+  int64_t c_batch_stride, c_row_stride;
+  int64_t z_batch_stride, z_row_stride;
+  int64_t y_batch_stride, y_row_stride;
+  int32_t dtype, batch, t_max, d, n;
+  int32_t dt_softplus;    /* 1: step = softplus(dt + dt_bias); 0: step = dt + dt_bias */
+} gam_scan_args;
+
+/* Selective state-space scan, for prompts and for single frames.  Per sequence
+ * and channel c, with state h [n] (state_in, or 0) and frames t in order:
+ *   s   = softplus(dt[t, c] + dt_bias[c])     (or without softplus)
+ *   h_i = exp(s a[c, i]) h_i + s x[t, c] b[t, i]
+ *   y[t, c] = (sum_i c[t, i] h_i + d_skip[c] x[t, c]) * z sigmoid(z),  z = z[t, c]
+ * n is 1 .. 64 (GAM_ERR_SHAPE).  Frames at or beyond a sequence's length are
+ * never read, leave the state alone and are written as zeros in y.  Arguments
+ * are DEVICE pointers in a HOST struct, which the call does not keep. */
+gam_status gam_selective_scan(const gam_scan_args* args, void* stream);
+
+/* Norm of gam_residual_norm: none, LayerNorm (weight and bias) or RMSNorm
+ * (weight). */
+enum { GAM_NORM_NONE = 0, GAM_NORM_LAYER = 1, GAM_NORM_RMS = 2 };
+
+/* Arguments of gam_residual_norm.  Strides in elements. */
+typedef struct {
+  const void* x;            /* x_dtype [rows, d]: residual stream                     */
+  const void* y;            /* dtype [rows, d]: the block's output                    */
+  const void* gate;         /* dtype [gate_rows, d], optional (no gate)               */
+  const float* layer_scale; /* f32 [d], optional (1)                                  */
+  const float* post_weight; /* f32 [d] (1 if NULL), norm of y                         */
+  const float* post_bias;   /* f32 [d] (0 if NULL; LayerNorm only)                    */
+  const float* pre_weight;  /* f32 [d] (1 if NULL), norm of the new residual          */
+  const float* pre_bias;    /* f32 [d] (0 if NULL; LayerNorm only)                    */
+  void* x_out;              /* x_dtype [rows, d], optional; may be x                  */
+  void* u;                  /* dtype [rows, d], optional; may be y                    */
+  int64_t x_stride, y_stride, gate_stride, x_out_stride, u_stride;
+  int64_t rows, gate_rows;  /* gate row r serves rows r * (rows / gate_rows) and on   */
+  int32_t x_dtype, dtype, d;
+  int32_t gate_act, post_norm, pre_norm;
+  float alpha, eps;
+} gam_residual_norm_args;
+
+/* Residual update with the norms around it, in one pass over the rows:
+ *   x' = x + alpha * layer_scale * gate_act(gate) * post_norm(y),  u = pre_norm(x')
+ * with LayerNorm(v) = (v - mean v) / sqrt(var v + eps) * weight + bias and
+ * RMSNorm(v) = v / sqrt(mean v^2 + eps) * weight over the d values of a row.
+ * x' is written to x_out, u to u (at least one of the two is given); u is taken
+ * from x' before its rounding to x_dtype.  x_dtype is dtype or GAM_DTYPE_F32.
+ * d 1 .. 16384 (GAM_ERR_CAPACITY above); rows is a multiple of gate_rows
+ * (GAM_ERR_SHAPE); rows are at least d apart; x_out may be x with x's stride and
+ * u may be y with y's stride. */
+gam_status gam_residual_norm(const gam_residual_norm_args* args, void* stream);
 
 /* ---- greedy decoding without any allocation ---- */
 
