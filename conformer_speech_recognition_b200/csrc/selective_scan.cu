@@ -92,37 +92,69 @@ __device__ __forceinline__ int length_of(const gam_scan_args& p, int b) {
 
 constexpr int kThreads = 128;
 
-// 8 neighbouring channels of a frame as they lie in memory; channels past d and
-// frames past the end are 0.
+// One value's bits, zero-extended: a load that nothing has to wait for before its use.
+__device__ __forceinline__ uint32_t load_bits(const float* p) { return __float_as_uint(*p); }
+__device__ __forceinline__ uint32_t load_bits(const __half* p) { return *reinterpret_cast<const unsigned short*>(p); }
+__device__ __forceinline__ uint32_t load_bits(const bf16* p) { return *reinterpret_cast<const unsigned short*>(p); }
 template <typename T>
-struct Raw {
-  T v[8];
-};
-template <typename T>
-__device__ __forceinline__ void load8(Raw<T>& r, const T* p, bool wide, bool on, int left) {
-  if (on && wide && left > 0) {
-    constexpr int V = 16 / sizeof(T);
-#pragma unroll
-    for (int i = 0; i < 8 / V; ++i) {
-      const Vec<T, V> q = *reinterpret_cast<const Vec<T, V>*>(p + i * V);
-#pragma unroll
-      for (int k = 0; k < V; ++k) r.v[i * V + k] = q.v[k];
-    }
-  } else {
-#pragma unroll
-    for (int k = 0; k < 8; ++k) r.v[k] = on && k < left ? p[k] : from_f<T>(0.f);
-  }
+__device__ __forceinline__ float from_bits(uint32_t u);
+template <>
+__device__ __forceinline__ float from_bits<float>(uint32_t u) { return __uint_as_float(u); }
+template <>
+__device__ __forceinline__ float from_bits<__half>(uint32_t u) {
+  return __half2float(__ushort_as_half((unsigned short)u));
 }
+template <>
+__device__ __forceinline__ float from_bits<bf16>(uint32_t u) { return __uint_as_float(u << 16); }
 
-template <typename T, int S, int L>
-__global__ void __launch_bounds__(kThreads) scan_kernel(const gam_scan_args p, const bool wide) {
+// 8 neighbouring channels of a frame as they lie in memory: 16-byte accesses where
+// WIDE (rows 16-byte aligned, d a multiple of 8), else value by value.  Channels
+// past d and frames past the end are 0.
+template <typename T, bool WIDE>
+struct Octet {
+  static constexpr int N = WIDE ? 8 * sizeof(T) / 16 : 8;
+  uint4 q[WIDE ? N : 1];
+  uint32_t u[WIDE ? 1 : N];
+  __device__ __forceinline__ void load(const T* p, bool on, int left) {
+    if constexpr (WIDE) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        q[i] = make_uint4(0, 0, 0, 0);
+        if (on) q[i] = *reinterpret_cast<const uint4*>(p + i * (16 / sizeof(T)));
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        u[i] = 0;
+        if (on && i < left) u[i] = load_bits(p + i);
+      }
+    }
+  }
+  __device__ __forceinline__ float get(int k) const {  // k known at compile time
+    if constexpr (!WIDE) {
+      return from_bits<T>(u[k]);
+    } else {
+      const uint4& v = q[k * sizeof(T) / 16];
+      const int w = k * sizeof(T) / 4 % 4;
+      const uint32_t word = w == 0 ? v.x : w == 1 ? v.y : w == 2 ? v.z : v.w;
+      if constexpr (sizeof(T) == 4) return from_bits<T>(word);
+      else return from_bits<T>((k & 1) ? word >> 16 : word & 0xffffu);
+    }
+  }
+};
+
+template <typename T, int S, int L, bool WIDE>
+__global__ void __launch_bounds__(kThreads) scan_kernel(const gam_scan_args p) {
   constexpr int CT = kThreads / L, TT = 1024 / CT, NP = S * L;
   constexpr int OCT = CT / 8;                        // groups of 8 channels in a row of the tile
   constexpr int BC = (TT * NP + kThreads - 1) / kThreads;  // values of b (and of c) a thread stages
-  __shared__ __align__(16) float2 s_in[TT][CT];      // s, s x
+  // (s, s x); the 16-byte chunk j of the 8 channels o lies at j ^ (o / 2) % 4, for the banks
+  __shared__ __align__(16) float2 s_in[TT][CT];
   __shared__ __align__(16) float s_b[TT][NP], s_c[TT][NP];
   __shared__ __align__(16) float s_y[TT][CT];
-  __shared__ float s_end[CT][NP + 1];                // a piece's end states and its sum of s
+  // per rank: the end states of its piece [CT][NP], then its sums of s [CT] (only in a cluster)
+  extern __shared__ __align__(16) float s_join[];
+  constexpr int JOIN = CT * (NP + 1);
   cg::cluster_group cluster = cg::this_cluster();
   const int R = cluster.num_blocks(), rank = cluster.block_rank();
   const int cblocks = (p.d + CT - 1) / CT;
@@ -154,7 +186,8 @@ __global__ void __launch_bounds__(kThreads) scan_kernel(const gam_scan_args p, c
   }
 
   // staging: thread -> frame tt of the tile, channels c8 .. c8 + 7
-  const int tt = tid / OCT, c8 = c0 + (tid % OCT) * 8, left = p.d - c8;
+  const int o8 = tid % OCT, tt = tid / OCT, c8 = c0 + o8 * 8, left = p.d - c8;
+  const int mine = (ch / 8 * 4 + ((ch % 8 / 2) ^ (ch / 16 % 4))) * 2 + ch % 2;  // this lane's channel in s_in
   const T* px = (const T*)p.x + b * p.x_batch_stride + c8;
   const T* pdt = (const T*)p.dt + b * p.dt_batch_stride + c8;
   const T* pz = p.z ? (const T*)p.z + b * p.z_batch_stride + c8 : nullptr;
@@ -171,82 +204,112 @@ __global__ void __launch_bounds__(kThreads) scan_kernel(const gam_scan_args p, c
   // One run over the piece; OUT: with outputs, else for the end state alone.
   auto pass = [&](auto out_tag, float& sum_s) {
     constexpr bool OUT = decltype(out_tag)::value;
-    Raw<T> x, dt, z, nx, ndt, nz;
-    T nb[BC], nc[BC];
+    Octet<T, WIDE> x, dt, z, nx, ndt, nz;
+    uint32_t nb[BC], nc[BC];
     auto fetch = [&](int t0) {
       const int t = t0 + tt;
-      const bool on = t < hi;
-      load8(nx, px + t * p.x_row_stride, wide, on, left);
-      load8(ndt, pdt + t * p.dt_row_stride, wide, on, left);
-      if (OUT && pz) load8(nz, pz + t * p.z_row_stride, wide, on, left);
+      const bool on = t < hi && left > 0;
+      nx.load(px + t * p.x_row_stride, on, left);
+      ndt.load(pdt + t * p.dt_row_stride, on, left);
+      if (OUT && pz) nz.load(pz + t * p.z_row_stride, on, left);
 #pragma unroll
       for (int i = 0; i < BC; ++i) {
         const int e = tid + i * kThreads, r = t0 + e / NP, k = e % NP;
         const bool use = e < TT * NP && r < hi && k < p.n;
-        nb[i] = use ? pb[r * p.b_row_stride + k] : from_f<T>(0.f);
-        if (OUT) nc[i] = use ? pc[r * p.c_row_stride + k] : from_f<T>(0.f);
+        nb[i] = nc[i] = 0;
+        if (use) nb[i] = load_bits(pb + r * p.b_row_stride + k);
+        if (OUT && use) nc[i] = load_bits(pc + r * p.c_row_stride + k);
       }
     };
     if (lo < hi) fetch(lo);
     for (int t0 = lo; t0 < hi; t0 += TT) {
       x = nx, dt = ndt;
-      if (OUT) z = nz;
+      if (OUT && pz) z = nz;
       const bool on = t0 + tt < hi;
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        float s = to_f(dt.v[k]) + bias[k];
-        if (p.dt_softplus) s = softplus_f(s);
-        if (!on) s = 0.f;                            // a frame past the end changes nothing
-        s_in[tt][(tid % OCT) * 8 + k] = make_float2(s, on ? s * to_f(x.v[k]) : 0.f);
+      for (int j = 0; j < 4; ++j) {
+        float4 q;
+        float s[2];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          s[k] = dt.get(2 * j + k) + bias[2 * j + k];
+          if (p.dt_softplus) s[k] = softplus_f(s[k]);
+          if (!on) s[k] = 0.f;                       // a frame past the end changes nothing: x is 0 there too
+        }
+        q = make_float4(s[0], s[0] * x.get(2 * j), s[1], s[1] * x.get(2 * j + 1));
+        *reinterpret_cast<float4*>(&s_in[tt][o8 * 8 + (j ^ (o8 / 2 % 4)) * 2]) = q;
       }
 #pragma unroll
       for (int i = 0; i < BC; ++i) {
         const int e = tid + i * kThreads;
         if (e < TT * NP) {
-          s_b[e / NP][e % NP] = to_f(nb[i]);
-          if (OUT) s_c[e / NP][e % NP] = to_f(nc[i]);
+          s_b[e / NP][e % NP] = from_bits<T>(nb[i]);
+          if (OUT) s_c[e / NP][e % NP] = from_bits<T>(nc[i]);
         }
       }
       __syncthreads();
       if (t0 + TT < hi) fetch(t0 + TT);
-#pragma unroll 4
-      for (int t = 0; t < TT; ++t) {
-        const float2 in = s_in[t][ch];
-        const u64 s2 = pack2(in.x, in.x), sx2 = pack2(in.y, in.y);
-        if (!OUT) sum_s += in.x;
-        u64 y2 = 0ull;
+#pragma unroll 1
+      for (int t4 = 0; t4 < TT; t4 += 4) {
+        float v[4];
 #pragma unroll
-        for (int i = 0; i < S / 4; ++i) {
-          const ulonglong2 bv = *reinterpret_cast<const ulonglong2*>(&s_b[t][part * S + 4 * i]);
-          ulonglong2 cv;
-          if (OUT) cv = *reinterpret_cast<const ulonglong2*>(&s_c[t][part * S + 4 * i]);
+        for (int f = 0; f < 4; ++f) {
+          const int t = t4 + f;
+          const float2 in = s_in[t][mine];
+          const u64 s2 = pack2(in.x, in.x), sx2 = pack2(in.y, in.y);
+          if (!OUT) sum_s += in.x;
+          u64 y2 = 0ull;
 #pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            const float2 e = unpack2(mul2(s2, a[2 * i + k]));
-            const u64 decay = pack2(exp2_approx(e.x), exp2_approx(e.y));
-            h[2 * i + k] = fma2(decay, h[2 * i + k], mul2(sx2, k ? bv.y : bv.x));
-            if (OUT) y2 = fma2(k ? cv.y : cv.x, h[2 * i + k], y2);
+          for (int i = 0; i < S / 4; ++i) {
+            const ulonglong2 bv = *reinterpret_cast<const ulonglong2*>(&s_b[t][part * S + 4 * i]);
+            ulonglong2 cv;
+            if (OUT) cv = *reinterpret_cast<const ulonglong2*>(&s_c[t][part * S + 4 * i]);
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              const float2 e = unpack2(mul2(s2, a[2 * i + k]));
+              const u64 decay = pack2(exp2_approx(e.x), exp2_approx(e.y));
+              h[2 * i + k] = fma2(decay, h[2 * i + k], mul2(sx2, k ? bv.y : bv.x));
+              if (OUT) y2 = i + k ? fma2(k ? cv.y : cv.x, h[2 * i + k], y2) : mul2(cv.x, h[0]);
+            }
           }
-        }
-        if (OUT) {
           const float2 yy = unpack2(y2);
-          float v = yy.x + yy.y;
+          if (OUT) v[f] = yy.x + yy.y;
+        }
+        if constexpr (OUT) {
+          // the lanes of a channel add their parts of 4 frames; with L >= 2 each ends with its own share of the frames
+          if constexpr (L == 1) {
 #pragma unroll
-          for (int o = L / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-          if (part == 0) s_y[t][ch] = v;
+            for (int f = 0; f < 4; ++f) s_y[t4 + f][ch] = v[f];
+          } else {
+            const bool up = part & 1;
+            float w[2];
+#pragma unroll
+            for (int f = 0; f < 2; ++f)
+              w[f] = (up ? v[f + 2] : v[f]) + __shfl_xor_sync(0xffffffffu, up ? v[f] : v[f + 2], 1);
+            if constexpr (L == 2) {
+#pragma unroll
+              for (int f = 0; f < 2; ++f) s_y[t4 + (up ? 2 : 0) + f][ch] = w[f];
+            } else {
+              const bool up2 = part & 2;
+              float q = (up2 ? w[1] : w[0]) + __shfl_xor_sync(0xffffffffu, up2 ? w[0] : w[1], 2);
+#pragma unroll
+              for (int o = 4; o < L; o <<= 1) q += __shfl_xor_sync(0xffffffffu, q, o);
+              if (part < 4) s_y[t4 + (up ? 2 : 0) + (up2 ? 1 : 0)][ch] = q;
+            }
+          }
         }
       }
       __syncthreads();
-      if (OUT && on) {
+      if (OUT && on && left > 0) {
         T o[8];
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
-          float v = fmaf(skip[k], to_f(x.v[k]), s_y[tt][(tid % OCT) * 8 + k]);
-          if (pz) v *= gate_f(to_f(z.v[k]));
+          float v = fmaf(skip[k], x.get(k), s_y[tt][o8 * 8 + k]);
+          if (pz) v *= gate_f(z.get(k));
           o[k] = from_f<T>(v);
         }
         T* dst = py + (t0 + tt) * p.y_row_stride;
-        if (wide && left > 0) {
+        if constexpr (WIDE) {
           constexpr int V = 16 / sizeof(T);
 #pragma unroll
           for (int i = 0; i < 8 / V; ++i) {
@@ -266,40 +329,36 @@ __global__ void __launch_bounds__(kThreads) scan_kernel(const gam_scan_args p, c
 
   float sum_s = 0.f;
   if (R > 1) {
-    if (rank > 0 && rank < R - 1) {
-      pass(std::false_type(), sum_s);
+    if (rank == 0) pass(std::true_type(), sum_s);    // the first piece knows its state
+    else if (rank < R - 1) pass(std::false_type(), sum_s);
+    cluster.sync();                                  // every CTA of the cluster has started: its shared memory is there
+    // to every later piece (stores over the cluster need no answer; loads were ten times slower)
+    for (int r = rank + 1; r < R; ++r) {
+      float* to = cluster.map_shared_rank(s_join, r) + rank * JOIN;
 #pragma unroll
-      for (int i = 0; i < S / 2; ++i) {
-        const float2 v = unpack2(h[i]);
-        s_end[ch][part * S + 2 * i] = v.x;
-        s_end[ch][part * S + 2 * i + 1] = v.y;
-      }
-      if (part == 0) s_end[ch][NP] = sum_s;
-    } else if (rank == 0) {
-      pass(std::true_type(), sum_s);                 // the first piece knows its state
-#pragma unroll
-      for (int i = 0; i < S / 2; ++i) {
-        const float2 v = unpack2(h[i]);
-        s_end[ch][part * S + 2 * i] = v.x;
-        s_end[ch][part * S + 2 * i + 1] = v.y;
-      }
+      for (int i = 0; i < S / 4; ++i)
+        *reinterpret_cast<ulonglong2*>(to + ch * NP + part * S + 4 * i) = make_ulonglong2(h[2 * i], h[2 * i + 1]);
+      if (part == 0) to[CT * NP + ch] = sum_s;
     }
     cluster.sync();
     if (rank > 0) {
       for (int r = 0; r < rank; ++r) {
-        const float* e = cluster.map_shared_rank(&s_end[ch][0], r);
-        const float q = r ? e[NP] : 0.f;             // the first piece's end state is whole already
+        const float* e = s_join + r * JOIN;
+        const float q = e[CT * NP + ch];
 #pragma unroll
-        for (int i = 0; i < S / 2; ++i) {
-          const float2 end = make_float2(e[part * S + 2 * i], e[part * S + 2 * i + 1]);
-          const float2 x2 = unpack2(mul2(pack2(q, q), a[i]));
-          const u64 before = r ? h[i] : 0ull;
-          h[i] = fma2(pack2(exp2_approx(x2.x), exp2_approx(x2.y)), before, pack2(end.x, end.y));
+        for (int i = 0; i < S / 4; ++i) {
+          const ulonglong2 end = *reinterpret_cast<const ulonglong2*>(e + ch * NP + part * S + 4 * i);
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const float2 x2 = unpack2(mul2(pack2(q, q), a[2 * i + k]));
+            const u64 decay = pack2(exp2_approx(x2.x), exp2_approx(x2.y));
+            // the first piece's end state is whole already
+            h[2 * i + k] = r ? fma2(decay, h[2 * i + k], k ? end.y : end.x) : (k ? end.y : end.x);
+          }
         }
       }
       pass(std::true_type(), sum_s);
     }
-    cluster.sync();                                  // shared memory stays until every reader is done
   } else {
     pass(std::true_type(), sum_s);
   }
@@ -421,13 +480,19 @@ gam_status launch_scan(const gam_scan_args& p, int sms, cudaStream_t s) {
   cfg.gridDim = dim3((unsigned)(ctas * R));
   cfg.blockDim = dim3(kThreads);
   cfg.stream = s;
+  cfg.dynamicSmemBytes = R > 1 ? (R - 1) * CT * (S * L + 1) * sizeof(float) : 0;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = R;
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return launch_status(cudaLaunchKernelEx(&cfg, scan_kernel<T, S, L>, p, wide));
+  auto kernel = wide ? scan_kernel<T, S, L, true> : scan_kernel<T, S, L, false>;
+  if (R > 1) {
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)cfg.dynamicSmemBytes);
+    if (e != cudaSuccess) return launch_status(e);
+  }
+  return launch_status(cudaLaunchKernelEx(&cfg, kernel, p));
 }
 
 template <typename T>
