@@ -82,7 +82,7 @@ __device__ __forceinline__ float softplus_f(float v) {
   q = fmaf(w2, q, 1.f / 5);
   q = fmaf(w2, q, 1.f / 3);
   q = fmaf(w2 * q, w, w);
-  return v != v ? v : fmaf(2.f, q, fmaxf(v, 0.f));
+  return fmaf(2.f, q, fmaxf(v, 0.f));  // a NaN comes through e
 }
 __device__ __forceinline__ float gate_f(float z) { return z * rcp_approx(1.f + exp2_approx(-z * kLog2e)); }
 
@@ -143,172 +143,249 @@ struct Octet {
   }
 };
 
-template <typename T, int S, int L, bool WIDE>
-__global__ void __launch_bounds__(kThreads) scan_kernel(const gam_scan_args p) {
-  constexpr int CT = kThreads / L, TT = 1024 / CT, NP = S * L;
+// 8 values from memory to shared memory, asynchronously; zeros where !on (nothing is read then).
+template <typename T>
+__device__ __forceinline__ void copy8(T* dst, const T* src, bool on) {
+  const uint32_t d = (uint32_t)__cvta_generic_to_shared(dst);
+  const int bytes = on ? 16 : 0;
+#pragma unroll
+  for (int i = 0; i < (int)sizeof(T) / 2; ++i)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(d + 16 * i),
+                 "l"(reinterpret_cast<const char*>(src) + 16 * i), "r"(bytes)
+                 : "memory");
+}
+
+template <typename T, int S, int L, int CH, bool WIDE>
+__global__ void __launch_bounds__(kThreads, CH == 2 ? 4 : 6) scan_kernel(const gam_scan_args p) {
+  constexpr int CT1 = kThreads / L, CT = CT1 * CH;   // a lane's channels are ch + j CT1, j < CH
+  constexpr int TT = 1024 / CT, NP = S * L;
   constexpr int OCT = CT / 8;                        // groups of 8 channels in a row of the tile
   constexpr int BC = (TT * NP + kThreads - 1) / kThreads;  // values of b (and of c) a thread stages
   // (s, s x); the 16-byte chunk j of the 8 channels o lies at j ^ (o / 2) % 4, for the banks
   __shared__ __align__(16) float2 s_in[TT][CT];
+  __shared__ __align__(16) float s_bias[CT], s_skip[CT];
   __shared__ __align__(16) float s_b[TT][NP], s_c[TT][NP];
   __shared__ __align__(16) float s_y[TT][CT];
+  extern __shared__ __align__(16) uint8_t s_dyn[];
+  // x, dt and z of this tile and the next as they lie in memory (WIDE); a thread reads only what it copied itself
+  auto raw = [&](int buf, int which) { return reinterpret_cast<T*>(s_dyn) + (buf * 3 + which) * 1024; };
   // per rank: the end states of its piece [CT][NP], then its sums of s [CT] (only in a cluster)
-  extern __shared__ __align__(16) float s_join[];
+  float* s_join = reinterpret_cast<float*>(s_dyn + (WIDE ? 6 * 1024 * sizeof(T) : 0));
   constexpr int JOIN = CT * (NP + 1);
   cg::cluster_group cluster = cg::this_cluster();
   const int R = cluster.num_blocks(), rank = cluster.block_rank();
   const int cblocks = (p.d + CT - 1) / CT;
   const int item = blockIdx.x / R;
-  const int cb = item % cblocks, b = item / cblocks, c0 = cb * CT;
   const int tid = threadIdx.x, part = tid % L, ch = tid / L;
+  // longest sequences first, so that the last CTAs to start are short ones: the one with `item / cblocks`
+  // longer (or equal and earlier) ones before it
+  __shared__ int s_seq;
+  if (p.lengths && p.batch > 1 && p.batch <= kThreads) {
+    if (tid < p.batch) {
+      const int mine = p.lengths[tid];
+      int before = 0;
+      for (int i = 0; i < p.batch; ++i) {
+        const int other = p.lengths[i];
+        before += other > mine || (other == mine && i < tid);
+      }
+      if (before == item / cblocks) s_seq = tid;
+    }
+    __syncthreads();
+  } else {
+    if (tid == 0) s_seq = item / cblocks;
+    __syncthreads();
+  }
+  const int cb = item % cblocks, b = s_seq, c0 = cb * CT;
   const int len = length_of(p, b);
   // this CTA's piece of the valid frames, whole tiles
   const int piece = ((len + R - 1) / R + TT - 1) / TT * TT;
   const int lo = min(rank * piece, len), hi = min(lo + piece, len);
 
-  const bool ch_on = c0 + ch < p.d;
-  const int cc = ch_on ? c0 + ch : p.d - 1;          // lanes past the last channel walk along, for the shuffles
-  u64 a[S / 2], h[S / 2];
+  // this lane's states in channel j: S from row (b, c), column part * S
+  auto channel = [&](int j) { return min(c0 + ch + j * CT1, p.d - 1); };  // lanes past the last channel walk along
+  u64 a[CH][S / 2], h[CH][S / 2];
 #pragma unroll
-  for (int i = 0; i < S / 2; ++i) {
-    const int k = part * S + 2 * i;
-    a[i] = pack2(k < p.n ? p.a[(int64_t)cc * p.n + k] * kLog2e : 0.f,
-                 k + 1 < p.n ? p.a[(int64_t)cc * p.n + k + 1] * kLog2e : 0.f);
-    h[i] = 0ull;
-  }
-  if (rank == 0 && p.state_in) {
-    const float* st = p.state_in + ((int64_t)b * p.d + cc) * p.n;
+  for (int j = 0; j < CH; ++j) {
+    const float* pa = p.a + (int64_t)channel(j) * p.n;
+    const float* st = rank == 0 && p.state_in ? p.state_in + ((int64_t)b * p.d + channel(j)) * p.n : nullptr;
 #pragma unroll
     for (int i = 0; i < S / 2; ++i) {
       const int k = part * S + 2 * i;
-      h[i] = pack2(k < p.n ? st[k] : 0.f, k + 1 < p.n ? st[k + 1] : 0.f);
+      a[j][i] = pack2(k < p.n ? pa[k] * kLog2e : 0.f, k + 1 < p.n ? pa[k + 1] * kLog2e : 0.f);
+      h[j][i] = pack2(st && k < p.n ? st[k] : 0.f, st && k + 1 < p.n ? st[k + 1] : 0.f);
     }
   }
 
   // staging: thread -> frame tt of the tile, channels c8 .. c8 + 7
   const int o8 = tid % OCT, tt = tid / OCT, c8 = c0 + o8 * 8, left = p.d - c8;
-  const int mine = (ch / 8 * 4 + ((ch % 8 / 2) ^ (ch / 16 % 4))) * 2 + ch % 2;  // this lane's channel in s_in
+  // a lane's channel j in s_in (CT1 is a multiple of 16; of 64 where it is above)
+  auto place = [&](int j) {
+    const int c = ch + j * CT1;
+    return (c / 8 * 4 + ((c % 8 / 2) ^ (c / 16 % 4))) * 2 + c % 2;
+  };
+  int mine[CH];
+#pragma unroll
+  for (int j = 0; j < CH; ++j) mine[j] = place(j);
   const T* px = (const T*)p.x + b * p.x_batch_stride + c8;
   const T* pdt = (const T*)p.dt + b * p.dt_batch_stride + c8;
   const T* pz = p.z ? (const T*)p.z + b * p.z_batch_stride + c8 : nullptr;
   const T* pb = (const T*)p.b + b * p.b_batch_stride;
   const T* pc = (const T*)p.c + b * p.c_batch_stride;
   T* py = (T*)p.y + b * p.y_batch_stride + c8;
-  float bias[8], skip[8];
-#pragma unroll
-  for (int k = 0; k < 8; ++k) {
-    bias[k] = p.dt_bias && k < left ? p.dt_bias[c8 + k] : 0.f;
-    skip[k] = p.d_skip && k < left ? p.d_skip[c8 + k] : 0.f;
+  if (tid < CT) {
+    const int c = c0 + tid;
+    s_bias[tid] = p.dt_bias && c < p.d ? p.dt_bias[c] : 0.f;
+    s_skip[tid] = p.d_skip && c < p.d ? p.d_skip[c] : 0.f;
   }
+  __syncthreads();
 
   // One run over the piece; OUT: with outputs, else for the end state alone.
-  auto pass = [&](auto out_tag, float& sum_s) {
+  auto pass = [&](auto out_tag, float (&sum_s)[CH]) {
     constexpr bool OUT = decltype(out_tag)::value;
-    Octet<T, WIDE> x, dt, z, nx, ndt, nz;
-    uint32_t nb[BC], nc[BC];
-    auto fetch = [&](int t0) {
+    constexpr bool AHEAD = BC <= 4;                  // b and c a tile ahead in registers
+    uint32_t nb[AHEAD ? BC : 1], nc[AHEAD ? BC : 1];
+    auto value_bc = [&](int t0, int e, uint32_t& vb, uint32_t& vc) {
+      const int r = t0 + e / NP, k = e % NP;
+      const bool use = e < TT * NP && r < hi && k < p.n;
+      vb = vc = 0;
+      if (use) vb = load_bits(pb + r * p.b_row_stride + k);
+      if (OUT && use) vc = load_bits(pc + r * p.c_row_stride + k);
+    };
+    auto fetch = [&](int t0, int buf) {
+      if constexpr (WIDE) {
+        const int t = t0 + tt;
+        const bool on = t < hi && left > 0;
+        copy8(raw(buf, 0) + tid * 8, px + t * p.x_row_stride, on);
+        copy8(raw(buf, 1) + tid * 8, pdt + t * p.dt_row_stride, on);
+        if (OUT && pz) copy8(raw(buf, 2) + tid * 8, pz + t * p.z_row_stride, on);
+        asm volatile("cp.async.commit_group;" ::: "memory");
+      }
+      if constexpr (AHEAD)
+#pragma unroll
+        for (int i = 0; i < BC; ++i) value_bc(t0, tid + i * kThreads, nb[i], nc[i]);
+    };
+    int buf = 0;
+    if (lo < hi) fetch(lo, 0);
+    for (int t0 = lo; t0 < hi; t0 += TT, buf ^= 1) {
       const int t = t0 + tt;
       const bool on = t < hi && left > 0;
-      nx.load(px + t * p.x_row_stride, on, left);
-      ndt.load(pdt + t * p.dt_row_stride, on, left);
-      if (OUT && pz) nz.load(pz + t * p.z_row_stride, on, left);
+      // 8 values of x (0), dt (1) or z (2) of this thread's frame
+      auto octet = [&](int which, const T* g) {
+        Octet<T, WIDE> r;
+        if constexpr (WIDE) r.load(raw(buf, which) + tid * 8, true, 8);
+        else r.load(g, on, left);
+        return r;
+      };
+      if (WIDE) asm volatile("cp.async.wait_group 0;" ::: "memory");
+      {
+        const Octet<T, WIDE> x = octet(0, px + t * p.x_row_stride), dt = octet(1, pdt + t * p.dt_row_stride);
 #pragma unroll
-      for (int i = 0; i < BC; ++i) {
-        const int e = tid + i * kThreads, r = t0 + e / NP, k = e % NP;
-        const bool use = e < TT * NP && r < hi && k < p.n;
-        nb[i] = nc[i] = 0;
-        if (use) nb[i] = load_bits(pb + r * p.b_row_stride + k);
-        if (OUT && use) nc[i] = load_bits(pc + r * p.c_row_stride + k);
-      }
-    };
-    if (lo < hi) fetch(lo);
-    for (int t0 = lo; t0 < hi; t0 += TT) {
-      x = nx, dt = ndt;
-      if (OUT && pz) z = nz;
-      const bool on = t0 + tt < hi;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        float4 q;
-        float s[2];
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          s[k] = dt.get(2 * j + k) + bias[2 * j + k];
-          if (p.dt_softplus) s[k] = softplus_f(s[k]);
-          if (!on) s[k] = 0.f;                       // a frame past the end changes nothing: x is 0 there too
+        for (int j = 0; j < 4; ++j) {
+          const float2 bias = *reinterpret_cast<const float2*>(&s_bias[o8 * 8 + 2 * j]);
+          float s0 = dt.get(2 * j) + bias.x, s1 = dt.get(2 * j + 1) + bias.y;
+          if (p.dt_softplus) s0 = softplus_f(s0), s1 = softplus_f(s1);
+          if (!on) s0 = s1 = 0.f;                    // a frame past the end changes nothing: x is 0 there too
+          *reinterpret_cast<float4*>(&s_in[tt][o8 * 8 + (j ^ (o8 / 2 % 4)) * 2]) =
+              make_float4(s0, s0 * x.get(2 * j), s1, s1 * x.get(2 * j + 1));
         }
-        q = make_float4(s[0], s[0] * x.get(2 * j), s[1], s[1] * x.get(2 * j + 1));
-        *reinterpret_cast<float4*>(&s_in[tt][o8 * 8 + (j ^ (o8 / 2 % 4)) * 2]) = q;
       }
+      if constexpr (AHEAD) {
 #pragma unroll
-      for (int i = 0; i < BC; ++i) {
-        const int e = tid + i * kThreads;
-        if (e < TT * NP) {
-          s_b[e / NP][e % NP] = from_bits<T>(nb[i]);
-          if (OUT) s_c[e / NP][e % NP] = from_bits<T>(nc[i]);
+        for (int i = 0; i < BC; ++i) {
+          const int e = tid + i * kThreads;
+          if (e < TT * NP) {
+            s_b[e / NP][e % NP] = from_bits<T>(nb[i]);
+            if (OUT) s_c[e / NP][e % NP] = from_bits<T>(nc[i]);
+          }
+        }
+      } else {
+#pragma unroll 4
+        for (int e = tid; e < TT * NP; e += kThreads) {
+          uint32_t vb, vc;
+          value_bc(t0, e, vb, vc);
+          s_b[e / NP][e % NP] = from_bits<T>(vb);
+          if (OUT) s_c[e / NP][e % NP] = from_bits<T>(vc);
         }
       }
       __syncthreads();
-      if (t0 + TT < hi) fetch(t0 + TT);
+      if (t0 + TT < hi) fetch(t0 + TT, buf ^ 1);
 #pragma unroll 1
       for (int t4 = 0; t4 < TT; t4 += 4) {
-        float v[4];
+        float v[CH][4];
 #pragma unroll
         for (int f = 0; f < 4; ++f) {
           const int t = t4 + f;
-          const float2 in = s_in[t][mine];
-          const u64 s2 = pack2(in.x, in.x), sx2 = pack2(in.y, in.y);
-          if (!OUT) sum_s += in.x;
-          u64 y2 = 0ull;
+          u64 s2[CH], sx2[CH], y2[CH];
+#pragma unroll
+          for (int j = 0; j < CH; ++j) {
+            const float2 in = s_in[t][mine[j]];
+            s2[j] = pack2(in.x, in.x), sx2[j] = pack2(in.y, in.y);
+            if (!OUT) sum_s[j] += in.x;
+          }
 #pragma unroll
           for (int i = 0; i < S / 4; ++i) {
             const ulonglong2 bv = *reinterpret_cast<const ulonglong2*>(&s_b[t][part * S + 4 * i]);
             ulonglong2 cv;
             if (OUT) cv = *reinterpret_cast<const ulonglong2*>(&s_c[t][part * S + 4 * i]);
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              const float2 e = unpack2(mul2(s2, a[2 * i + k]));
-              const u64 decay = pack2(exp2_approx(e.x), exp2_approx(e.y));
-              h[2 * i + k] = fma2(decay, h[2 * i + k], mul2(sx2, k ? bv.y : bv.x));
-              if (OUT) y2 = i + k ? fma2(k ? cv.y : cv.x, h[2 * i + k], y2) : mul2(cv.x, h[0]);
-            }
+            for (int k = 0; k < 2; ++k)
+#pragma unroll
+              for (int j = 0; j < CH; ++j) {
+                u64& hh = h[j][2 * i + k];
+                const float2 e = unpack2(mul2(s2[j], a[j][2 * i + k]));
+                const u64 decay = pack2(exp2_approx(e.x), exp2_approx(e.y));
+                hh = fma2(decay, hh, mul2(sx2[j], k ? bv.y : bv.x));
+                if (OUT) y2[j] = i + k ? fma2(k ? cv.y : cv.x, hh, y2[j]) : mul2(cv.x, hh);
+              }
           }
-          const float2 yy = unpack2(y2);
-          if (OUT) v[f] = yy.x + yy.y;
+          if (OUT)
+#pragma unroll
+            for (int j = 0; j < CH; ++j) {
+              const float2 yy = unpack2(y2[j]);
+              v[j][f] = yy.x + yy.y;
+            }
         }
         if constexpr (OUT) {
           // the lanes of a channel add their parts of 4 frames; with L >= 2 each ends with its own share of the frames
-          if constexpr (L == 1) {
 #pragma unroll
-            for (int f = 0; f < 4; ++f) s_y[t4 + f][ch] = v[f];
-          } else {
-            const bool up = part & 1;
-            float w[2];
+          for (int j = 0; j < CH; ++j) {
+            const int c = ch + j * CT1;
+            if constexpr (L == 1) {
 #pragma unroll
-            for (int f = 0; f < 2; ++f)
-              w[f] = (up ? v[f + 2] : v[f]) + __shfl_xor_sync(0xffffffffu, up ? v[f] : v[f + 2], 1);
-            if constexpr (L == 2) {
-#pragma unroll
-              for (int f = 0; f < 2; ++f) s_y[t4 + (up ? 2 : 0) + f][ch] = w[f];
+              for (int f = 0; f < 4; ++f) s_y[t4 + f][c] = v[j][f];
             } else {
-              const bool up2 = part & 2;
-              float q = (up2 ? w[1] : w[0]) + __shfl_xor_sync(0xffffffffu, up2 ? w[0] : w[1], 2);
+              const bool up = part & 1;
+              float w[2];
 #pragma unroll
-              for (int o = 4; o < L; o <<= 1) q += __shfl_xor_sync(0xffffffffu, q, o);
-              if (part < 4) s_y[t4 + (up ? 2 : 0) + (up2 ? 1 : 0)][ch] = q;
+              for (int f = 0; f < 2; ++f)
+                w[f] = (up ? v[j][f + 2] : v[j][f]) + __shfl_xor_sync(0xffffffffu, up ? v[j][f] : v[j][f + 2], 1);
+              if constexpr (L == 2) {
+#pragma unroll
+                for (int f = 0; f < 2; ++f) s_y[t4 + (up ? 2 : 0) + f][c] = w[f];
+              } else {
+                const bool up2 = part & 2;
+                float q = (up2 ? w[1] : w[0]) + __shfl_xor_sync(0xffffffffu, up2 ? w[0] : w[1], 2);
+#pragma unroll
+                for (int o = 4; o < L; o <<= 1) q += __shfl_xor_sync(0xffffffffu, q, o);
+                if (part < 4) s_y[t4 + (up ? 2 : 0) + (up2 ? 1 : 0)][c] = q;
+              }
             }
           }
         }
       }
       __syncthreads();
-      if (OUT && on && left > 0) {
+      if (OUT && on) {
+        const Octet<T, WIDE> x = octet(0, px + t * p.x_row_stride);
+        Octet<T, WIDE> z;
+        if (pz) z = octet(2, pz + t * p.z_row_stride);
         T o[8];
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
-          float v = fmaf(skip[k], x.get(k), s_y[tt][o8 * 8 + k]);
+          float v = fmaf(s_skip[o8 * 8 + k], x.get(k), s_y[tt][o8 * 8 + k]);
           if (pz) v *= gate_f(z.get(k));
           o[k] = from_f<T>(v);
         }
-        T* dst = py + (t0 + tt) * p.y_row_stride;
+        T* dst = py + t * p.y_row_stride;
         if constexpr (WIDE) {
           constexpr int V = 16 / sizeof(T);
 #pragma unroll
@@ -327,7 +404,7 @@ __global__ void __launch_bounds__(kThreads) scan_kernel(const gam_scan_args p) {
     }
   };
 
-  float sum_s = 0.f;
+  float sum_s[CH] = {};
   if (R > 1) {
     if (rank == 0) pass(std::true_type(), sum_s);    // the first piece knows its state
     else if (rank < R - 1) pass(std::false_type(), sum_s);
@@ -336,24 +413,33 @@ __global__ void __launch_bounds__(kThreads) scan_kernel(const gam_scan_args p) {
     for (int r = rank + 1; r < R; ++r) {
       float* to = cluster.map_shared_rank(s_join, r) + rank * JOIN;
 #pragma unroll
-      for (int i = 0; i < S / 4; ++i)
-        *reinterpret_cast<ulonglong2*>(to + ch * NP + part * S + 4 * i) = make_ulonglong2(h[2 * i], h[2 * i + 1]);
-      if (part == 0) to[CT * NP + ch] = sum_s;
+      for (int j = 0; j < CH; ++j) {
+        const int c = ch + j * CT1;
+#pragma unroll
+        for (int i = 0; i < S / 4; ++i)
+          *reinterpret_cast<ulonglong2*>(to + c * NP + part * S + 4 * i) = make_ulonglong2(h[j][2 * i], h[j][2 * i + 1]);
+        if (part == 0) to[CT * NP + c] = sum_s[j];
+      }
     }
     cluster.sync();
     if (rank > 0) {
       for (int r = 0; r < rank; ++r) {
         const float* e = s_join + r * JOIN;
-        const float q = e[CT * NP + ch];
 #pragma unroll
-        for (int i = 0; i < S / 4; ++i) {
-          const ulonglong2 end = *reinterpret_cast<const ulonglong2*>(e + ch * NP + part * S + 4 * i);
+        for (int j = 0; j < CH; ++j) {
+          const int c = ch + j * CT1;
+          const float q = e[CT * NP + c];
 #pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            const float2 x2 = unpack2(mul2(pack2(q, q), a[2 * i + k]));
-            const u64 decay = pack2(exp2_approx(x2.x), exp2_approx(x2.y));
-            // the first piece's end state is whole already
-            h[2 * i + k] = r ? fma2(decay, h[2 * i + k], k ? end.y : end.x) : (k ? end.y : end.x);
+          for (int i = 0; i < S / 4; ++i) {
+            const ulonglong2 end = *reinterpret_cast<const ulonglong2*>(e + c * NP + part * S + 4 * i);
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              u64& hh = h[j][2 * i + k];
+              const float2 x2 = unpack2(mul2(pack2(q, q), a[j][2 * i + k]));
+              const u64 decay = pack2(exp2_approx(x2.x), exp2_approx(x2.y));
+              // the first piece's end state is whole already
+              hh = r ? fma2(decay, hh, k ? end.y : end.x) : (k ? end.y : end.x);
+            }
           }
         }
       }
@@ -363,14 +449,19 @@ __global__ void __launch_bounds__(kThreads) scan_kernel(const gam_scan_args p) {
     pass(std::true_type(), sum_s);
   }
 
-  if (rank == R - 1 && p.state_out && ch_on) {
-    float* st = p.state_out + ((int64_t)b * p.d + cc) * p.n;
+  if (rank == R - 1 && p.state_out) {
 #pragma unroll
-    for (int i = 0; i < S / 2; ++i) {
-      const int k = part * S + 2 * i;
-      const float2 v = unpack2(h[i]);
-      if (k < p.n) st[k] = v.x;
-      if (k + 1 < p.n) st[k + 1] = v.y;
+    for (int j = 0; j < CH; ++j) {
+      const int c = c0 + ch + j * CT1;
+      if (c >= p.d) continue;
+      float* st = p.state_out + ((int64_t)b * p.d + c) * p.n;
+#pragma unroll
+      for (int i = 0; i < S / 2; ++i) {
+        const int k = part * S + 2 * i;
+        const float2 v = unpack2(h[j][i]);
+        if (k < p.n) st[k] = v.x;
+        if (k + 1 < p.n) st[k + 1] = v.y;
+      }
     }
   }
   // frames behind the end are zero
@@ -462,13 +553,14 @@ gam_status launch_step(const gam_scan_args& p, cudaStream_t s) {
   return launch_status(cudaGetLastError());
 }
 
-template <typename T, int S, int L>
+template <typename T, int S, int L, int CH>
 gam_status launch_scan(const gam_scan_args& p, int sms, cudaStream_t s) {
-  constexpr int CT = kThreads / L, TT = 1024 / CT;
+  constexpr int CT = kThreads / L * CH, TT = 1024 / CT;
   const int64_t ctas = (int64_t)((p.d + CT - 1) / CT) * p.batch;
-  // split while the pieces keep two tiles and the CTAs do not fill the SMs four times
+  // split while the pieces keep two tiles and the CTAs do not fill the SMs
   int R = 1;
-  while (R < 8 && ctas * R * 2 <= (int64_t)sms * 4 && p.t_max >= R * 2 * 2 * TT) R *= 2;
+  if (CH == 1)
+    while (R < 8 && ctas * R * 2 <= (int64_t)sms * 4 && p.t_max >= R * 2 * 2 * TT) R *= 2;
   if (R == 2) R = 1;                                 // twice the work for twice the SMs gains nothing
   if (ctas * R > INT32_MAX) return op_fail(GAM_ERR_CAPACITY, "batch * d too large for one call");
   constexpr int V = 16 / sizeof(T);
@@ -480,19 +572,29 @@ gam_status launch_scan(const gam_scan_args& p, int sms, cudaStream_t s) {
   cfg.gridDim = dim3((unsigned)(ctas * R));
   cfg.blockDim = dim3(kThreads);
   cfg.stream = s;
-  cfg.dynamicSmemBytes = R > 1 ? (R - 1) * CT * (S * L + 1) * sizeof(float) : 0;
+  cfg.dynamicSmemBytes = (wide ? 6 * 1024 * sizeof(T) : 0) + (R - 1) * CT * (S * L + 1) * sizeof(float);
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = R;
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  auto kernel = wide ? scan_kernel<T, S, L, true> : scan_kernel<T, S, L, false>;
-  if (R > 1) {
+  auto kernel = wide ? scan_kernel<T, S, L, CH, true> : scan_kernel<T, S, L, CH, false>;
+  constexpr int kFixed = 1024 * 8 + TT * S * L * 8 + 1024 * 4 + CT * 8 + 64;  // the kernel's static shared memory
+  if (cfg.dynamicSmemBytes + kFixed > 48 * 1024) {
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)cfg.dynamicSmemBytes);
     if (e != cudaSuccess) return launch_status(e);
   }
   return launch_status(cudaLaunchKernelEx(&cfg, kernel, p));
+}
+
+// Lanes with two channels of S states where that still gives every SM work, else
+// lanes with one channel of S1 states, and a cluster over the time axis.
+template <typename T, int S, int L, int S1, int L1>
+gam_status launch_pair(const gam_scan_args& p, int sms, cudaStream_t s) {
+  constexpr int CT = kThreads / L * 2;
+  const int64_t ctas = (int64_t)((p.d + CT - 1) / CT) * p.batch;
+  return ctas >= 2 * sms ? launch_scan<T, S, L, 2>(p, sms, s) : launch_scan<T, S1, L1, 1>(p, sms, s);
 }
 
 template <typename T>
@@ -504,11 +606,11 @@ gam_status launch(const gam_scan_args& p, int sms, cudaStream_t s) {
     if (p.n <= 32) return launch_step<T, 8>(p, s);
     return launch_step<T, 16>(p, s);
   }
-  if (p.n <= 4) return launch_scan<T, 4, 1>(p, sms, s);
-  if (p.n <= 8) return launch_scan<T, 8, 1>(p, sms, s);
-  if (p.n <= 16) return launch_scan<T, 8, 2>(p, sms, s);
-  if (p.n <= 32) return launch_scan<T, 8, 4>(p, sms, s);
-  return launch_scan<T, 16, 4>(p, sms, s);
+  if (p.n <= 4) return launch_scan<T, 4, 1, 1>(p, sms, s);
+  if (p.n <= 8) return launch_pair<T, 8, 1, 4, 2>(p, sms, s);
+  if (p.n <= 16) return launch_pair<T, 8, 2, 4, 4>(p, sms, s);
+  if (p.n <= 32) return launch_pair<T, 8, 4, 4, 8>(p, sms, s);
+  return launch_pair<T, 8, 8, 8, 8>(p, sms, s);
 }
 
 }  // namespace
