@@ -6,10 +6,10 @@
 // element by element, so the bound is the exponentials (16 per clock and SM), then
 // the fp32 multiply-adds; the bytes come far behind for 16 states and more.
 //
-// Frames in numbers (scan_kernel): a CTA takes 128 / L channels of one sequence;
-// L neighbouring lanes share a channel and hold S states each in registers (S L
-// >= n; states past n have a = b = c = 0).  Time goes in tiles of 8 L frames, 1024
-// (frame, channel) pairs, 8 neighbouring channels of a frame to a thread: it
+// Frames in numbers (scan_kernel): a CTA takes 64 / L channels (or twice as many) of
+// one sequence; L neighbouring lanes share a channel and hold S states each in registers (S L
+// >= n; states past n have a = b = c = 0).  Time goes in tiles of 512 (frame,
+// channel) pairs, 8 neighbouring channels of a frame to a thread: it
 // fetches them one tile ahead in 16-byte accesses, forms s and s x once for the L
 // lanes, and later applies skip and gate to the y the lanes have left in shared
 // memory.  Inside a tile the lanes only read shared memory and their registers;
@@ -59,10 +59,19 @@ __device__ __forceinline__ u64 mul2(u64 a, u64 b) {
   asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
 }
+__device__ __forceinline__ u64 add2(u64 a, u64 b) {
+  u64 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
 __device__ __forceinline__ float exp2_approx(float v) {
   float r;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
   return r;
+}
+__device__ __forceinline__ u64 exp2_approx2(u64 v) {
+  const float2 e = unpack2(v);
+  return pack2(exp2_approx(e.x), exp2_approx(e.y));
 }
 __device__ __forceinline__ float rcp_approx(float v) {
   float r;
@@ -70,27 +79,33 @@ __device__ __forceinline__ float rcp_approx(float v) {
   return r;
 }
 
-// log(1 + e^v) = max(v, 0) + log1p(e), e = e^-|v| in (0, 1].  log1p(e) = 2 atanh(w)
-// with w = e / (2 + e) <= 1/3, by its series to w^13: the rest is below 2 w^15 / 15,
-// 1.5e-8 of the sum, and nothing cancels, so small steps keep their digits.
-__device__ __forceinline__ float softplus_f(float v) {
-  const float e = exp2_approx(-fabsf(v) * kLog2e);
-  const float w = e * rcp_approx(2.f + e), w2 = w * w;
-  float q = fmaf(w2, 1.f / 13, 1.f / 11);
-  q = fmaf(w2, q, 1.f / 9);
-  q = fmaf(w2, q, 1.f / 7);
-  q = fmaf(w2, q, 1.f / 5);
-  q = fmaf(w2, q, 1.f / 3);
-  q = fmaf(w2 * q, w, w);
-  return fmaf(2.f, q, fmaxf(v, 0.f));  // a NaN comes through e
+__device__ __forceinline__ u64 both(float v) { return pack2(v, v); }
+
+// log(1 + e^v) = max(v, 0) + log1p(e), e = e^-|v| in (0, 1], for two values.  log1p(e) / e
+// by the polynomial of degree 8 with the least largest relative error on [0, 1] (3e-8;
+// 1.7e-7 evaluated in fp32): nothing cancels, so small steps keep their digits.
+// A NaN comes through e.
+__device__ __forceinline__ float2 softplus2(float2 v) {
+  const u64 e = pack2(exp2_approx(-fabsf(v.x) * kLog2e), exp2_approx(-fabsf(v.y) * kLog2e));
+  u64 q = both(0.0052326930941379795f);
+  q = fma2(q, e, both(-0.02950523979961872f));
+  q = fma2(q, e, both(0.07822595536708832f));
+  q = fma2(q, e, both(-0.13663245737552643f));
+  q = fma2(q, e, both(0.19106006622314453f));
+  q = fma2(q, e, both(-0.2484298199415207f));
+  q = fma2(q, e, both(0.3331909775733948f));
+  q = fma2(q, e, both(-0.4999949336051941f));
+  q = fma2(q, e, both(0.9999999403953552f));
+  return unpack2(fma2(q, e, pack2(fmaxf(v.x, 0.f), fmaxf(v.y, 0.f))));
 }
+__device__ __forceinline__ float softplus_f(float v) { return softplus2(make_float2(v, 0.f)).x; }
 __device__ __forceinline__ float gate_f(float z) { return z * rcp_approx(1.f + exp2_approx(-z * kLog2e)); }
 
 __device__ __forceinline__ int length_of(const gam_scan_args& p, int b) {
   return p.lengths ? min(max(p.lengths[b], 0), p.t_max) : p.t_max;
 }
 
-constexpr int kThreads = 128;
+constexpr int kThreads = 64, kTile = kThreads * 8;  // threads of a CTA, (frame, channel) pairs of a tile
 
 // One value's bits, zero-extended: a load that nothing has to wait for before its use.
 __device__ __forceinline__ uint32_t load_bits(const float* p) { return __float_as_uint(*p); }
@@ -143,6 +158,23 @@ struct Octet {
   }
 };
 
+__device__ __forceinline__ void store8(float* p, const float (&v)[8]) {
+  reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
+  reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+}
+__device__ __forceinline__ void store8(__half* p, const float (&v)[8]) {
+  Vec<__half2, 4> q;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) q.v[i] = __floats2half2_rn(v[2 * i], v[2 * i + 1]);
+  *reinterpret_cast<Vec<__half2, 4>*>(p) = q;
+}
+__device__ __forceinline__ void store8(bf16* p, const float (&v)[8]) {
+  Vec<__nv_bfloat162, 4> q;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) q.v[i] = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+  *reinterpret_cast<Vec<__nv_bfloat162, 4>*>(p) = q;
+}
+
 // 8 values from memory to shared memory, asynchronously; zeros where !on (nothing is read then).
 template <typename T>
 __device__ __forceinline__ void copy8(T* dst, const T* src, bool on) {
@@ -155,12 +187,19 @@ __device__ __forceinline__ void copy8(T* dst, const T* src, bool on) {
                  : "memory");
 }
 
+// The first `bytes` (0 .. 4) of 4 bytes, zeros behind them.
+template <typename T>
+__device__ __forceinline__ void copy4(T* dst, const T* src, int bytes) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src),
+               "r"(bytes)
+               : "memory");
+}
+
 template <typename T, int S, int L, int CH, bool WIDE>
-__global__ void __launch_bounds__(kThreads, CH == 2 ? 4 : 6) scan_kernel(const gam_scan_args p) {
+__global__ void __launch_bounds__(kThreads, CH == 2 ? 8 : 12) scan_kernel(const gam_scan_args p, const int sms, const bool pair) {
   constexpr int CT1 = kThreads / L, CT = CT1 * CH;   // a lane's channels are ch + j CT1, j < CH
-  constexpr int TT = 1024 / CT, NP = S * L;
+  constexpr int TT = kTile / CT, NP = S * L;
   constexpr int OCT = CT / 8;                        // groups of 8 channels in a row of the tile
-  constexpr int BC = (TT * NP + kThreads - 1) / kThreads;  // values of b (and of c) a thread stages
   // (s, s x); the 16-byte chunk j of the 8 channels o lies at j ^ (o / 2) % 4, for the banks
   __shared__ __align__(16) float2 s_in[TT][CT];
   __shared__ __align__(16) float s_bias[CT], s_skip[CT];
@@ -168,34 +207,41 @@ __global__ void __launch_bounds__(kThreads, CH == 2 ? 4 : 6) scan_kernel(const g
   __shared__ __align__(16) float s_y[TT][CT];
   extern __shared__ __align__(16) uint8_t s_dyn[];
   // x, dt and z of this tile and the next as they lie in memory (WIDE); a thread reads only what it copied itself
-  auto raw = [&](int buf, int which) { return reinterpret_cast<T*>(s_dyn) + (buf * 3 + which) * 1024; };
+  auto raw = [&](int buf, int which) { return reinterpret_cast<T*>(s_dyn) + (buf * 3 + which) * kTile; };
+  // b and c likewise (PAIR: their rows 4-byte aligned), two 16-bit values or one of 32 bits to a copy
+  constexpr int PER = 4 / sizeof(T);
+  auto raw_bc = [&](int buf, int which) {
+    return reinterpret_cast<T*>(s_dyn) + (WIDE ? 6 * kTile : 0) + (buf * 2 + which) * TT * NP;
+  };
   // per rank: the end states of its piece [CT][NP], then its sums of s [CT] (only in a cluster)
-  float* s_join = reinterpret_cast<float*>(s_dyn + (WIDE ? 6 * 1024 * sizeof(T) : 0));
+  float* s_join = reinterpret_cast<float*>(s_dyn + ((WIDE ? 6 * kTile : 0) + (pair ? 4 * TT * NP : 0)) * sizeof(T));
   constexpr int JOIN = CT * (NP + 1);
   cg::cluster_group cluster = cg::this_cluster();
   const int R = cluster.num_blocks(), rank = cluster.block_rank();
   const int cblocks = (p.d + CT - 1) / CT;
   const int item = blockIdx.x / R;
   const int tid = threadIdx.x, part = tid % L, ch = tid / L;
-  // longest sequences first, so that the last CTAs to start are short ones: the one with `item / cblocks`
-  // longer (or equal and earlier) ones before it
+  // Longest sequences first, in rounds of one CTA to an SM that run to and fro, so that an SM whose
+  // first piece of work is long gets a short second one: sequence b has `before` longer ones.
   __shared__ int s_seq;
-  if (p.lengths && p.batch > 1 && p.batch <= kThreads) {
-    if (tid < p.batch) {
-      const int mine = p.lengths[tid];
+  int place_of = item;
+  if (p.lengths && p.batch > 1 && p.batch <= 256) {
+    const int items = cblocks * p.batch, round = item / sms, left_over = items - round * sms;
+    if (round & 1) place_of = round * sms + min(sms, left_over) - 1 - item % sms;
+    for (int i = tid; i < p.batch; i += kThreads) {
+      const int own = p.lengths[i];
       int before = 0;
-      for (int i = 0; i < p.batch; ++i) {
-        const int other = p.lengths[i];
-        before += other > mine || (other == mine && i < tid);
+      for (int k = 0; k < p.batch; ++k) {
+        const int other = p.lengths[k];
+        before += other > own || (other == own && k < i);
       }
-      if (before == item / cblocks) s_seq = tid;
+      if (before == place_of / cblocks) s_seq = i;
     }
-    __syncthreads();
-  } else {
-    if (tid == 0) s_seq = item / cblocks;
-    __syncthreads();
+  } else if (tid == 0) {
+    s_seq = item / cblocks;
   }
-  const int cb = item % cblocks, b = s_seq, c0 = cb * CT;
+  __syncthreads();
+  const int cb = place_of % cblocks, b = s_seq, c0 = cb * CT;
   const int len = length_of(p, b);
   // this CTA's piece of the valid frames, whole tiles
   const int piece = ((len + R - 1) / R + TT - 1) / TT * TT;
@@ -242,15 +288,6 @@ __global__ void __launch_bounds__(kThreads, CH == 2 ? 4 : 6) scan_kernel(const g
   // One run over the piece; OUT: with outputs, else for the end state alone.
   auto pass = [&](auto out_tag, float (&sum_s)[CH]) {
     constexpr bool OUT = decltype(out_tag)::value;
-    constexpr bool AHEAD = BC <= 4;                  // b and c a tile ahead in registers
-    uint32_t nb[AHEAD ? BC : 1], nc[AHEAD ? BC : 1];
-    auto value_bc = [&](int t0, int e, uint32_t& vb, uint32_t& vc) {
-      const int r = t0 + e / NP, k = e % NP;
-      const bool use = e < TT * NP && r < hi && k < p.n;
-      vb = vc = 0;
-      if (use) vb = load_bits(pb + r * p.b_row_stride + k);
-      if (OUT && use) vc = load_bits(pc + r * p.c_row_stride + k);
-    };
     auto fetch = [&](int t0, int buf) {
       if constexpr (WIDE) {
         const int t = t0 + tt;
@@ -258,11 +295,17 @@ __global__ void __launch_bounds__(kThreads, CH == 2 ? 4 : 6) scan_kernel(const g
         copy8(raw(buf, 0) + tid * 8, px + t * p.x_row_stride, on);
         copy8(raw(buf, 1) + tid * 8, pdt + t * p.dt_row_stride, on);
         if (OUT && pz) copy8(raw(buf, 2) + tid * 8, pz + t * p.z_row_stride, on);
-        asm volatile("cp.async.commit_group;" ::: "memory");
       }
-      if constexpr (AHEAD)
-#pragma unroll
-        for (int i = 0; i < BC; ++i) value_bc(t0, tid + i * kThreads, nb[i], nc[i]);
+      if (pair) {
+#pragma unroll 4
+        for (int e = tid * PER; e < TT * NP; e += kThreads * PER) {
+          const int r = t0 + e / NP, k = e % NP;
+          const int bytes = r < hi && k < p.n ? min(4, (p.n - k) * (int)sizeof(T)) : 0;  // the rest of the 4 is zero
+          copy4(raw_bc(buf, 0) + e, bytes ? pb + r * p.b_row_stride + k : pb, bytes);
+          if (OUT) copy4(raw_bc(buf, 1) + e, bytes ? pc + r * p.c_row_stride + k : pc, bytes);
+        }
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
     };
     int buf = 0;
     if (lo < hi) fetch(lo, 0);
@@ -276,33 +319,35 @@ __global__ void __launch_bounds__(kThreads, CH == 2 ? 4 : 6) scan_kernel(const g
         else r.load(g, on, left);
         return r;
       };
-      if (WIDE) asm volatile("cp.async.wait_group 0;" ::: "memory");
+      asm volatile("cp.async.wait_group 0;" ::: "memory");
       {
         const Octet<T, WIDE> x = octet(0, px + t * p.x_row_stride), dt = octet(1, pdt + t * p.dt_row_stride);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const float2 bias = *reinterpret_cast<const float2*>(&s_bias[o8 * 8 + 2 * j]);
-          float s0 = dt.get(2 * j) + bias.x, s1 = dt.get(2 * j + 1) + bias.y;
-          if (p.dt_softplus) s0 = softplus_f(s0), s1 = softplus_f(s1);
-          if (!on) s0 = s1 = 0.f;                    // a frame past the end changes nothing: x is 0 there too
+          float2 st = make_float2(dt.get(2 * j) + bias.x, dt.get(2 * j + 1) + bias.y);
+          if (p.dt_softplus) st = softplus2(st);
+          if (!on) st = make_float2(0.f, 0.f);       // a frame past the end changes nothing: x is 0 there too
           *reinterpret_cast<float4*>(&s_in[tt][o8 * 8 + (j ^ (o8 / 2 % 4)) * 2]) =
-              make_float4(s0, s0 * x.get(2 * j), s1, s1 * x.get(2 * j + 1));
+              make_float4(st.x, st.x * x.get(2 * j), st.y, st.y * x.get(2 * j + 1));
         }
       }
-      if constexpr (AHEAD) {
+      if (pair) {
+#pragma unroll 4
+        for (int e = tid * PER; e < TT * NP; e += kThreads * PER)
 #pragma unroll
-        for (int i = 0; i < BC; ++i) {
-          const int e = tid + i * kThreads;
-          if (e < TT * NP) {
-            s_b[e / NP][e % NP] = from_bits<T>(nb[i]);
-            if (OUT) s_c[e / NP][e % NP] = from_bits<T>(nc[i]);
+          for (int i = 0; i < PER; ++i) {
+            s_b[e / NP][e % NP + i] = to_f(raw_bc(buf, 0)[e + i]);
+            if (OUT) s_c[e / NP][e % NP + i] = to_f(raw_bc(buf, 1)[e + i]);
           }
-        }
       } else {
 #pragma unroll 4
         for (int e = tid; e < TT * NP; e += kThreads) {
-          uint32_t vb, vc;
-          value_bc(t0, e, vb, vc);
+          const int r = t0 + e / NP, k = e % NP;
+          const bool use = r < hi && k < p.n;
+          uint32_t vb = 0, vc = 0;
+          if (use) vb = load_bits(pb + r * p.b_row_stride + k);
+          if (OUT && use) vc = load_bits(pc + r * p.c_row_stride + k);
           s_b[e / NP][e % NP] = from_bits<T>(vb);
           if (OUT) s_c[e / NP][e % NP] = from_bits<T>(vc);
         }
@@ -332,8 +377,8 @@ __global__ void __launch_bounds__(kThreads, CH == 2 ? 4 : 6) scan_kernel(const g
 #pragma unroll
               for (int j = 0; j < CH; ++j) {
                 u64& hh = h[j][2 * i + k];
-                const float2 e = unpack2(mul2(s2[j], a[j][2 * i + k]));
-                const u64 decay = pack2(exp2_approx(e.x), exp2_approx(e.y));
+                const u64 e = mul2(s2[j], a[j][2 * i + k]);
+                const u64 decay = exp2_approx2(e);
                 hh = fma2(decay, hh, mul2(sx2[j], k ? bv.y : bv.x));
                 if (OUT) y2[j] = i + k ? fma2(k ? cv.y : cv.x, hh, y2[j]) : mul2(cv.x, hh);
               }
@@ -378,27 +423,19 @@ __global__ void __launch_bounds__(kThreads, CH == 2 ? 4 : 6) scan_kernel(const g
         const Octet<T, WIDE> x = octet(0, px + t * p.x_row_stride);
         Octet<T, WIDE> z;
         if (pz) z = octet(2, pz + t * p.z_row_stride);
-        T o[8];
+        float o[8];
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
-          float v = fmaf(s_skip[o8 * 8 + k], x.get(k), s_y[tt][o8 * 8 + k]);
-          if (pz) v *= gate_f(z.get(k));
-          o[k] = from_f<T>(v);
+          o[k] = fmaf(s_skip[o8 * 8 + k], x.get(k), s_y[tt][o8 * 8 + k]);
+          if (pz) o[k] *= gate_f(z.get(k));
         }
         T* dst = py + t * p.y_row_stride;
         if constexpr (WIDE) {
-          constexpr int V = 16 / sizeof(T);
-#pragma unroll
-          for (int i = 0; i < 8 / V; ++i) {
-            Vec<T, V> q;
-#pragma unroll
-            for (int k = 0; k < V; ++k) q.v[k] = o[i * V + k];
-            *reinterpret_cast<Vec<T, V>*>(dst + i * V) = q;
-          }
+          store8(dst, o);
         } else {
 #pragma unroll
           for (int k = 0; k < 8; ++k)
-            if (k < left) dst[k] = o[k];
+            if (k < left) dst[k] = from_f<T>(o[k]);
         }
       }
     }
@@ -555,12 +592,12 @@ gam_status launch_step(const gam_scan_args& p, cudaStream_t s) {
 
 template <typename T, int S, int L, int CH>
 gam_status launch_scan(const gam_scan_args& p, int sms, cudaStream_t s) {
-  constexpr int CT = kThreads / L * CH, TT = 1024 / CT;
+  constexpr int CT = kThreads / L * CH, TT = kTile / CT;
   const int64_t ctas = (int64_t)((p.d + CT - 1) / CT) * p.batch;
   // split while the pieces keep two tiles and the CTAs do not fill the SMs
   int R = 1;
   if (CH == 1)
-    while (R < 8 && ctas * R * 2 <= (int64_t)sms * 4 && p.t_max >= R * 2 * 2 * TT) R *= 2;
+    while (R < 8 && ctas * R * 2 <= (int64_t)sms * 8 && p.t_max >= R * 2 * 2 * TT) R *= 2;
   if (R == 2) R = 1;                                 // twice the work for twice the SMs gains nothing
   if (ctas * R > INT32_MAX) return op_fail(GAM_ERR_CAPACITY, "batch * d too large for one call");
   constexpr int V = 16 / sizeof(T);
@@ -572,7 +609,10 @@ gam_status launch_scan(const gam_scan_args& p, int sms, cudaStream_t s) {
   cfg.gridDim = dim3((unsigned)(ctas * R));
   cfg.blockDim = dim3(kThreads);
   cfg.stream = s;
-  cfg.dynamicSmemBytes = (wide ? 6 * 1024 * sizeof(T) : 0) + (R - 1) * CT * (S * L + 1) * sizeof(float);
+  constexpr int PER = 4 / sizeof(T);
+  const bool pair = aligned(p.b, 4) && aligned(p.c, 4) && p.b_batch_stride % PER == 0 && p.b_row_stride % PER == 0 &&
+                    p.c_batch_stride % PER == 0 && p.c_row_stride % PER == 0;
+  cfg.dynamicSmemBytes = (pair ? 4 * TT * S * L * sizeof(T) : 0) + (wide ? 6 * kTile * sizeof(T) : 0) + (R - 1) * CT * (S * L + 1) * sizeof(float);
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = R;
@@ -580,12 +620,12 @@ gam_status launch_scan(const gam_scan_args& p, int sms, cudaStream_t s) {
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   auto kernel = wide ? scan_kernel<T, S, L, CH, true> : scan_kernel<T, S, L, CH, false>;
-  constexpr int kFixed = 1024 * 8 + TT * S * L * 8 + 1024 * 4 + CT * 8 + 64;  // the kernel's static shared memory
+  constexpr int kFixed = kTile * 8 + TT * S * L * 8 + kTile * 4 + CT * 8 + 1024 + 64;  // static and reserved shared memory
   if (cfg.dynamicSmemBytes + kFixed > 48 * 1024) {
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)cfg.dynamicSmemBytes);
     if (e != cudaSuccess) return launch_status(e);
   }
-  return launch_status(cudaLaunchKernelEx(&cfg, kernel, p));
+  return launch_status(cudaLaunchKernelEx(&cfg, kernel, p, sms, pair));
 }
 
 // Lanes with two channels of S states where that still gives every SM work, else
@@ -594,7 +634,7 @@ template <typename T, int S, int L, int S1, int L1>
 gam_status launch_pair(const gam_scan_args& p, int sms, cudaStream_t s) {
   constexpr int CT = kThreads / L * 2;
   const int64_t ctas = (int64_t)((p.d + CT - 1) / CT) * p.batch;
-  return ctas >= 2 * sms ? launch_scan<T, S, L, 2>(p, sms, s) : launch_scan<T, S1, L1, 1>(p, sms, s);
+  return ctas >= 4 * sms ? launch_scan<T, S, L, 2>(p, sms, s) : launch_scan<T, S1, L1, 1>(p, sms, s);
 }
 
 template <typename T>
