@@ -105,7 +105,7 @@ __device__ __forceinline__ int length_of(const gam_scan_args& p, int b) {
   return p.lengths ? min(max(p.lengths[b], 0), p.t_max) : p.t_max;
 }
 
-constexpr int kThreads = 64, kTile = kThreads * 8;  // threads of a CTA, (frame, channel) pairs of a tile
+constexpr int kLanes = 64, kTile = kLanes * 8;  // lanes of a CTA, (frame, channel) pairs of a tile at most
 
 // One value's bits, zero-extended: a load that nothing has to wait for before its use.
 __device__ __forceinline__ uint32_t load_bits(const float* p) { return __float_as_uint(*p); }
@@ -195,40 +195,60 @@ __device__ __forceinline__ void copy4(T* dst, const T* src, int bytes) {
                : "memory");
 }
 
+// Frames of a tile: 8 channels of a frame to each producer, and at most 1024 values of b.
+constexpr int tile_frames(int CT, int NP) { return kTile / CT < 1024 / NP ? kTile / CT : 1024 / NP; }
+
+template <typename T, int S, int L, int CH>
+struct ScanShape {
+  static constexpr bool SPLIT = CH == 1;                 // producers beside the lanes
+  static constexpr int THREADS = SPLIT ? 2 * kLanes : kLanes;
+  static constexpr int CT1 = kLanes / L, CT = CT1 * CH;  // channels of a CTA: a lane's are ch + j CT1, j < CH
+  static constexpr int NP = S * L, TT = tile_frames(CT, NP);
+  static constexpr int JOIN = CT * (NP + 1);             // a piece's end states [CT][NP] and its sums of s [CT]
+  // shared memory: copies as they lie in memory, then two tiles of (s, s x), b, c and y; the pieces' end
+  // states take the tiles' place between two runs
+  static constexpr int RAW = 9 * kTile * sizeof(T), RAW_BC = 4 * TT * NP * sizeof(T);
+  static constexpr int TILES = 2 * TT * (CT * 3 + NP * 2) * sizeof(float);
+  static size_t bytes(bool wide, bool pair, int R) {
+    const int join = (R - 1) * JOIN * (int)sizeof(float);
+    return (wide ? RAW : 0) + (pair ? RAW_BC : 0) + (join > TILES ? join : TILES);
+  }
+};
+
 template <typename T, int S, int L, int CH, bool WIDE>
-__global__ void __launch_bounds__(kThreads, CH == 2 ? 8 : 12) scan_kernel(const gam_scan_args p, const int sms, const bool pair) {
-  constexpr int CT1 = kThreads / L, CT = CT1 * CH;   // a lane's channels are ch + j CT1, j < CH
-  constexpr int TT = kTile / CT, NP = S * L;
+__global__ void __launch_bounds__(ScanShape<T, S, L, CH>::THREADS, ScanShape<T, S, L, CH>::SPLIT ? 6 : 8)
+scan_kernel(const gam_scan_args p, const int sms, const bool pair) {
+  using Shape = ScanShape<T, S, L, CH>;
+  constexpr int CT1 = Shape::CT1, CT = Shape::CT, TT = Shape::TT, NP = Shape::NP, JOIN = Shape::JOIN;
   constexpr int OCT = CT / 8;                        // groups of 8 channels in a row of the tile
-  // (s, s x); the 16-byte chunk j of the 8 channels o lies at j ^ (o / 2) % 4, for the banks
-  __shared__ __align__(16) float2 s_in[TT][CT];
+  constexpr int PER = 4 / sizeof(T);                 // values of b in 4 bytes
+  constexpr bool SPLIT = Shape::SPLIT;
+  constexpr int kThreads = Shape::THREADS;
   __shared__ __align__(16) float s_bias[CT], s_skip[CT];
-  __shared__ __align__(16) float s_b[TT][NP], s_c[TT][NP];
-  __shared__ __align__(16) float s_y[TT][CT];
+  __shared__ int s_seq;
   extern __shared__ __align__(16) uint8_t s_dyn[];
-  // x, dt and z of this tile and the next as they lie in memory (WIDE); a thread reads only what it copied itself
-  auto raw = [&](int buf, int which) { return reinterpret_cast<T*>(s_dyn) + (buf * 3 + which) * kTile; };
-  // b and c likewise (PAIR: their rows 4-byte aligned), two 16-bit values or one of 32 bits to a copy
-  constexpr int PER = 4 / sizeof(T);
-  auto raw_bc = [&](int buf, int which) {
-    return reinterpret_cast<T*>(s_dyn) + (WIDE ? 6 * kTile : 0) + (buf * 2 + which) * TT * NP;
-  };
-  // per rank: the end states of its piece [CT][NP], then its sums of s [CT] (only in a cluster)
-  float* s_join = reinterpret_cast<float*>(s_dyn + ((WIDE ? 6 * kTile : 0) + (pair ? 4 * TT * NP : 0)) * sizeof(T));
-  constexpr int JOIN = CT * (NP + 1);
+  // x, dt and z of three tiles as they lie in memory (WIDE), b and c of two (pair: their rows are 4-byte
+  // aligned); a thread reads only what it copied itself
+  T* const s_raw = reinterpret_cast<T*>(s_dyn);
+  T* const s_raw_bc = reinterpret_cast<T*>(s_dyn + (WIDE ? Shape::RAW : 0));
+  uint8_t* const s_tiles = s_dyn + (WIDE ? Shape::RAW : 0) + (pair ? Shape::RAW_BC : 0);
+  // two tiles each: (s, s x), the 16-byte chunk j of the 8 channels o at j ^ (o / 2) % 4 for the banks; y; b; c
+  float2(*const s_in)[TT][CT] = reinterpret_cast<float2(*)[TT][CT]>(s_tiles);
+  float(*const s_y)[TT][CT] = reinterpret_cast<float(*)[TT][CT]>(s_tiles + 2 * TT * CT * 8);
+  float(*const s_b)[TT][NP] = reinterpret_cast<float(*)[TT][NP]>(s_tiles + 2 * TT * CT * 12);
+  float(*const s_c)[TT][NP] = s_b + 2;
+  float* const s_join = reinterpret_cast<float*>(s_tiles);  // [rank][JOIN], in a cluster
   cg::cluster_group cluster = cg::this_cluster();
   const int R = cluster.num_blocks(), rank = cluster.block_rank();
   const int cblocks = (p.d + CT - 1) / CT;
   const int item = blockIdx.x / R;
-  const int tid = threadIdx.x, part = tid % L, ch = tid / L;
   // Longest sequences first, in rounds of one CTA to an SM that run to and fro, so that an SM whose
   // first piece of work is long gets a short second one: sequence b has `before` longer ones.
-  __shared__ int s_seq;
   int place_of = item;
   if (p.lengths && p.batch > 1 && p.batch <= 256) {
     const int items = cblocks * p.batch, round = item / sms, left_over = items - round * sms;
     if (round & 1) place_of = round * sms + min(sms, left_over) - 1 - item % sms;
-    for (int i = tid; i < p.batch; i += kThreads) {
+    for (int i = threadIdx.x; i < p.batch; i += kThreads) {
       const int own = p.lengths[i];
       int before = 0;
       for (int k = 0; k < p.batch; ++k) {
@@ -237,19 +257,171 @@ __global__ void __launch_bounds__(kThreads, CH == 2 ? 8 : 12) scan_kernel(const 
       }
       if (before == place_of / cblocks) s_seq = i;
     }
-  } else if (tid == 0) {
+  } else if (threadIdx.x == 0) {
     s_seq = item / cblocks;
   }
+  const int cb = place_of % cblocks, c0 = cb * CT;
+  for (int i = threadIdx.x; i < CT; i += kThreads) {
+    s_bias[i] = p.dt_bias && c0 + i < p.d ? p.dt_bias[c0 + i] : 0.f;
+    s_skip[i] = p.d_skip && c0 + i < p.d ? p.d_skip[c0 + i] : 0.f;
+  }
   __syncthreads();
-  const int cb = place_of % cblocks, b = s_seq, c0 = cb * CT;
-  const int len = length_of(p, b);
+  const int b = s_seq, len = length_of(p, b);
   // this CTA's piece of the valid frames, whole tiles
   const int piece = ((len + R - 1) / R + TT - 1) / TT * TT;
   const int lo = min(rank * piece, len), hi = min(lo + piece, len);
+  const int tiles = (hi - lo + TT - 1) / TT;
 
-  // this lane's states in channel j: S from row (b, c), column part * S
+  // ---- producers: 8 neighbouring channels of one frame of each tile ----
+    const int tid = threadIdx.x % kLanes, o8 = tid % OCT, tt = tid / OCT, left = p.d - c0 - o8 * 8;
+    const bool mine = tt < TT && left > 0;
+    const int64_t at = c0 + o8 * 8;
+    const T* px = (const T*)p.x + b * p.x_batch_stride + at;
+    const T* pdt = (const T*)p.dt + b * p.dt_batch_stride + at;
+    const T* pz = p.z ? (const T*)p.z + b * p.z_batch_stride + at : nullptr;
+    const T* pb = (const T*)p.b + b * p.b_batch_stride;
+    const T* pc = (const T*)p.c + b * p.c_batch_stride;
+    T* py = (T*)p.y + b * p.y_batch_stride + at;
+    auto fetch = [&](auto out_tag, int k) {          // tile k on its way
+        constexpr bool OUT = decltype(out_tag)::value;
+        const int t0 = lo + k * TT, t = t0 + tt;
+        if (k < tiles) {
+          if constexpr (WIDE) {
+            T* raw = s_raw + k % 3 * 3 * kTile + tid * 8;
+            const bool on = mine && t < hi;
+            copy8(raw, px + (on ? t * p.x_row_stride : 0), on);
+            copy8(raw + kTile, pdt + (on ? t * p.dt_row_stride : 0), on);
+            if (OUT && pz) copy8(raw + 2 * kTile, pz + (on ? t * p.z_row_stride : 0), on);
+          }
+          if (pair) {
+            T* raw = s_raw_bc + (k & 1) * 2 * TT * NP;
+#pragma unroll 4
+            for (int e = tid * PER; e < TT * NP; e += kLanes * PER) {
+              const int r = t0 + e / NP, i = e % NP;
+              const int bytes = r < hi && i < p.n ? min(4, (p.n - i) * (int)sizeof(T)) : 0;  // the rest of the 4 is zero
+              copy4(raw + e, bytes ? pb + r * p.b_row_stride + i : pb, bytes);
+              if (OUT) copy4(raw + TT * NP + e, bytes ? pc + r * p.c_row_stride + i : pc, bytes);
+            }
+          }
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+      };
+      // 8 values of x (0), dt (1) or z (2) of this thread's frame of tile k
+      auto octet = [&](int k, int which, const T* g) {
+        Octet<T, WIDE> r;
+        if constexpr (WIDE) r.load(s_raw + (k % 3 * 3 + which) * kTile + tid * 8, true, 8);
+        else r.load(g, mine && lo + k * TT + tt < hi, left);
+        return r;
+      };
+      auto prepare = [&](auto out_tag, int k) {      // s, s x, b and c of tile k
+        constexpr bool OUT = decltype(out_tag)::value;
+        const int t0 = lo + k * TT, t = t0 + tt;
+        if (tt < TT) {
+          const bool on = mine && t < hi;
+          const Octet<T, WIDE> x = octet(k, 0, px + t * p.x_row_stride), dt = octet(k, 1, pdt + t * p.dt_row_stride);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float2 bias = *reinterpret_cast<const float2*>(&s_bias[o8 * 8 + 2 * j]);
+            float2 st = make_float2(dt.get(2 * j) + bias.x, dt.get(2 * j + 1) + bias.y);
+            if (p.dt_softplus) st = softplus2(st);
+            if (!on) st = make_float2(0.f, 0.f);     // a frame past the end changes nothing: x is 0 there too
+            *reinterpret_cast<float4*>(&s_in[k & 1][tt][o8 * 8 + (j ^ (o8 / 2 % 4)) * 2]) =
+                make_float4(st.x, st.x * x.get(2 * j), st.y, st.y * x.get(2 * j + 1));
+          }
+        }
+        float* const db = &s_b[k & 1][0][0];
+        float* const dc = &s_c[k & 1][0][0];
+        if (pair) {
+          const T* raw = s_raw_bc + (k & 1) * 2 * TT * NP;
+#pragma unroll 4
+          for (int e = tid * PER; e < TT * NP; e += kLanes * PER)
+#pragma unroll
+            for (int i = 0; i < PER; ++i) {
+              db[e + i] = to_f(raw[e + i]);
+              if (OUT) dc[e + i] = to_f(raw[TT * NP + e + i]);
+            }
+        } else {
+#pragma unroll 4
+          for (int e = tid; e < TT * NP; e += kLanes) {
+            const int r = t0 + e / NP, i = e % NP;
+            const bool use = r < hi && i < p.n;
+            uint32_t vb = 0, vc = 0;
+            if (use) vb = load_bits(pb + r * p.b_row_stride + i);
+            if (OUT && use) vc = load_bits(pc + r * p.c_row_stride + i);
+            db[e] = from_bits<T>(vb);
+            if (OUT) dc[e] = from_bits<T>(vc);
+          }
+        }
+      };
+      auto finish = [&](int k) {                     // skip and gate, and out
+        const int t = lo + k * TT + tt;
+        if (!mine || t >= hi) return;
+        const Octet<T, WIDE> x = octet(k, 0, px + t * p.x_row_stride);
+        Octet<T, WIDE> z;
+        if (pz) z = octet(k, 2, pz + t * p.z_row_stride);
+        float o[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          o[i] = fmaf(s_skip[o8 * 8 + i], x.get(i), s_y[k & 1][tt][o8 * 8 + i]);
+          if (pz) o[i] *= gate_f(z.get(i));
+        }
+        T* dst = py + t * p.y_row_stride;
+        if constexpr (WIDE) {
+          store8(dst, o);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            if (i < left) dst[i] = from_f<T>(o[i]);
+        }
+      };
+    auto zeros = [&] {                               // frames behind the end
+      if (mine)
+        for (int t = len + rank * TT + tt; t < p.t_max; t += R * TT) {
+          T* dst = py + t * p.y_row_stride;
+          if constexpr (WIDE) {
+            store8(dst, {});
+          } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              if (i < left) dst[i] = from_f<T>(0.f);
+          }
+        }
+    };
+    if (SPLIT && threadIdx.x >= kLanes) {
+      // while the lanes run tile k: the y of the one before goes out, the one after is made ready
+      auto pass = [&](auto out_tag) {
+        constexpr bool OUT = decltype(out_tag)::value;
+        fetch(out_tag, 0);
+        fetch(out_tag, 1);
+        asm volatile("cp.async.wait_group 1;" ::: "memory");
+        if (tiles > 0) prepare(out_tag, 0);
+        __syncthreads();
+        for (int k = 0; k < tiles; ++k) {
+          if (OUT && k > 0) finish(k - 1);
+          fetch(out_tag, k + 2);
+          asm volatile("cp.async.wait_group 1;" ::: "memory");
+          if (k + 1 < tiles) prepare(out_tag, k + 1);
+          __syncthreads();
+        }
+        if (OUT && tiles > 0) finish(tiles - 1);
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
+      };
+      if (R == 1 || rank == 0) pass(std::true_type());
+      else if (rank < R - 1) pass(std::false_type());
+      if (R > 1) {
+        cluster.sync();
+        cluster.sync();
+        if (rank > 0) pass(std::true_type());
+      }
+      zeros();
+      return;
+    }
+
+  // ---- lanes: the recurrence ----
+  const int part = tid % L, ch = tid / L;
   auto channel = [&](int j) { return min(c0 + ch + j * CT1, p.d - 1); };  // lanes past the last channel walk along
   u64 a[CH][S / 2], h[CH][S / 2];
+  int col[CH];                                       // channel j's place in a row of s_in
 #pragma unroll
   for (int j = 0; j < CH; ++j) {
     const float* pa = p.a + (int64_t)channel(j) * p.n;
@@ -260,100 +432,14 @@ __global__ void __launch_bounds__(kThreads, CH == 2 ? 8 : 12) scan_kernel(const 
       a[j][i] = pack2(k < p.n ? pa[k] * kLog2e : 0.f, k + 1 < p.n ? pa[k + 1] * kLog2e : 0.f);
       h[j][i] = pack2(st && k < p.n ? st[k] : 0.f, st && k + 1 < p.n ? st[k + 1] : 0.f);
     }
-  }
-
-  // staging: thread -> frame tt of the tile, channels c8 .. c8 + 7
-  const int o8 = tid % OCT, tt = tid / OCT, c8 = c0 + o8 * 8, left = p.d - c8;
-  // a lane's channel j in s_in (CT1 is a multiple of 16; of 64 where it is above)
-  auto place = [&](int j) {
     const int c = ch + j * CT1;
-    return (c / 8 * 4 + ((c % 8 / 2) ^ (c / 16 % 4))) * 2 + c % 2;
-  };
-  int mine[CH];
-#pragma unroll
-  for (int j = 0; j < CH; ++j) mine[j] = place(j);
-  const T* px = (const T*)p.x + b * p.x_batch_stride + c8;
-  const T* pdt = (const T*)p.dt + b * p.dt_batch_stride + c8;
-  const T* pz = p.z ? (const T*)p.z + b * p.z_batch_stride + c8 : nullptr;
-  const T* pb = (const T*)p.b + b * p.b_batch_stride;
-  const T* pc = (const T*)p.c + b * p.c_batch_stride;
-  T* py = (T*)p.y + b * p.y_batch_stride + c8;
-  if (tid < CT) {
-    const int c = c0 + tid;
-    s_bias[tid] = p.dt_bias && c < p.d ? p.dt_bias[c] : 0.f;
-    s_skip[tid] = p.d_skip && c < p.d ? p.d_skip[c] : 0.f;
+    col[j] = (c / 8 * 4 + ((c % 8 / 2) ^ (c / 16 % 4))) * 2 + c % 2;
   }
-  __syncthreads();
-
-  // One run over the piece; OUT: with outputs, else for the end state alone.
-  auto pass = [&](auto out_tag, float (&sum_s)[CH]) {
+  float sum_s[CH] = {};
+  // The lanes' work on tile k; OUT: with outputs, else for the end state and the sum of s alone.
+  auto run = [&](auto out_tag, int k) {
     constexpr bool OUT = decltype(out_tag)::value;
-    auto fetch = [&](int t0, int buf) {
-      if constexpr (WIDE) {
-        const int t = t0 + tt;
-        const bool on = t < hi && left > 0;
-        copy8(raw(buf, 0) + tid * 8, px + t * p.x_row_stride, on);
-        copy8(raw(buf, 1) + tid * 8, pdt + t * p.dt_row_stride, on);
-        if (OUT && pz) copy8(raw(buf, 2) + tid * 8, pz + t * p.z_row_stride, on);
-      }
-      if (pair) {
-#pragma unroll 4
-        for (int e = tid * PER; e < TT * NP; e += kThreads * PER) {
-          const int r = t0 + e / NP, k = e % NP;
-          const int bytes = r < hi && k < p.n ? min(4, (p.n - k) * (int)sizeof(T)) : 0;  // the rest of the 4 is zero
-          copy4(raw_bc(buf, 0) + e, bytes ? pb + r * p.b_row_stride + k : pb, bytes);
-          if (OUT) copy4(raw_bc(buf, 1) + e, bytes ? pc + r * p.c_row_stride + k : pc, bytes);
-        }
-      }
-      asm volatile("cp.async.commit_group;" ::: "memory");
-    };
-    int buf = 0;
-    if (lo < hi) fetch(lo, 0);
-    for (int t0 = lo; t0 < hi; t0 += TT, buf ^= 1) {
-      const int t = t0 + tt;
-      const bool on = t < hi && left > 0;
-      // 8 values of x (0), dt (1) or z (2) of this thread's frame
-      auto octet = [&](int which, const T* g) {
-        Octet<T, WIDE> r;
-        if constexpr (WIDE) r.load(raw(buf, which) + tid * 8, true, 8);
-        else r.load(g, on, left);
-        return r;
-      };
-      asm volatile("cp.async.wait_group 0;" ::: "memory");
-      {
-        const Octet<T, WIDE> x = octet(0, px + t * p.x_row_stride), dt = octet(1, pdt + t * p.dt_row_stride);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float2 bias = *reinterpret_cast<const float2*>(&s_bias[o8 * 8 + 2 * j]);
-          float2 st = make_float2(dt.get(2 * j) + bias.x, dt.get(2 * j + 1) + bias.y);
-          if (p.dt_softplus) st = softplus2(st);
-          if (!on) st = make_float2(0.f, 0.f);       // a frame past the end changes nothing: x is 0 there too
-          *reinterpret_cast<float4*>(&s_in[tt][o8 * 8 + (j ^ (o8 / 2 % 4)) * 2]) =
-              make_float4(st.x, st.x * x.get(2 * j), st.y, st.y * x.get(2 * j + 1));
-        }
-      }
-      if (pair) {
-#pragma unroll 4
-        for (int e = tid * PER; e < TT * NP; e += kThreads * PER)
-#pragma unroll
-          for (int i = 0; i < PER; ++i) {
-            s_b[e / NP][e % NP + i] = to_f(raw_bc(buf, 0)[e + i]);
-            if (OUT) s_c[e / NP][e % NP + i] = to_f(raw_bc(buf, 1)[e + i]);
-          }
-      } else {
-#pragma unroll 4
-        for (int e = tid; e < TT * NP; e += kThreads) {
-          const int r = t0 + e / NP, k = e % NP;
-          const bool use = r < hi && k < p.n;
-          uint32_t vb = 0, vc = 0;
-          if (use) vb = load_bits(pb + r * p.b_row_stride + k);
-          if (OUT && use) vc = load_bits(pc + r * p.c_row_stride + k);
-          s_b[e / NP][e % NP] = from_bits<T>(vb);
-          if (OUT) s_c[e / NP][e % NP] = from_bits<T>(vc);
-        }
-      }
-      __syncthreads();
-      if (t0 + TT < hi) fetch(t0 + TT, buf ^ 1);
+    const int buf = k & 1;
 #pragma unroll 1
       for (int t4 = 0; t4 < TT; t4 += 4) {
         float v[CH][4];
@@ -363,24 +449,23 @@ __global__ void __launch_bounds__(kThreads, CH == 2 ? 8 : 12) scan_kernel(const 
           u64 s2[CH], sx2[CH], y2[CH];
 #pragma unroll
           for (int j = 0; j < CH; ++j) {
-            const float2 in = s_in[t][mine[j]];
-            s2[j] = pack2(in.x, in.x), sx2[j] = pack2(in.y, in.y);
+            const float2 in = s_in[buf][t][col[j]];
+            s2[j] = both(in.x), sx2[j] = both(in.y);
             if (!OUT) sum_s[j] += in.x;
           }
 #pragma unroll
           for (int i = 0; i < S / 4; ++i) {
-            const ulonglong2 bv = *reinterpret_cast<const ulonglong2*>(&s_b[t][part * S + 4 * i]);
+            const ulonglong2 bv = *reinterpret_cast<const ulonglong2*>(&s_b[buf][t][part * S + 4 * i]);
             ulonglong2 cv;
-            if (OUT) cv = *reinterpret_cast<const ulonglong2*>(&s_c[t][part * S + 4 * i]);
+            if (OUT) cv = *reinterpret_cast<const ulonglong2*>(&s_c[buf][t][part * S + 4 * i]);
 #pragma unroll
-            for (int k = 0; k < 2; ++k)
+            for (int q = 0; q < 2; ++q)
 #pragma unroll
               for (int j = 0; j < CH; ++j) {
-                u64& hh = h[j][2 * i + k];
-                const u64 e = mul2(s2[j], a[j][2 * i + k]);
-                const u64 decay = exp2_approx2(e);
-                hh = fma2(decay, hh, mul2(sx2[j], k ? bv.y : bv.x));
-                if (OUT) y2[j] = i + k ? fma2(k ? cv.y : cv.x, hh, y2[j]) : mul2(cv.x, hh);
+                u64& hh = h[j][2 * i + q];
+                const u64 decay = exp2_approx2(mul2(s2[j], a[j][2 * i + q]));
+                hh = fma2(decay, hh, mul2(sx2[j], q ? bv.y : bv.x));
+                if (OUT) y2[j] = i + q ? fma2(q ? cv.y : cv.x, hh, y2[j]) : mul2(cv.x, hh);
               }
           }
           if (OUT)
@@ -397,7 +482,7 @@ __global__ void __launch_bounds__(kThreads, CH == 2 ? 8 : 12) scan_kernel(const 
             const int c = ch + j * CT1;
             if constexpr (L == 1) {
 #pragma unroll
-              for (int f = 0; f < 4; ++f) s_y[t4 + f][c] = v[j][f];
+              for (int f = 0; f < 4; ++f) s_y[buf][t4 + f][c] = v[j][f];
             } else {
               const bool up = part & 1;
               float w[2];
@@ -406,45 +491,50 @@ __global__ void __launch_bounds__(kThreads, CH == 2 ? 8 : 12) scan_kernel(const 
                 w[f] = (up ? v[j][f + 2] : v[j][f]) + __shfl_xor_sync(0xffffffffu, up ? v[j][f] : v[j][f + 2], 1);
               if constexpr (L == 2) {
 #pragma unroll
-                for (int f = 0; f < 2; ++f) s_y[t4 + (up ? 2 : 0) + f][c] = w[f];
+                for (int f = 0; f < 2; ++f) s_y[buf][t4 + (up ? 2 : 0) + f][c] = w[f];
               } else {
                 const bool up2 = part & 2;
                 float q = (up2 ? w[1] : w[0]) + __shfl_xor_sync(0xffffffffu, up2 ? w[0] : w[1], 2);
 #pragma unroll
                 for (int o = 4; o < L; o <<= 1) q += __shfl_xor_sync(0xffffffffu, q, o);
-                if (part < 4) s_y[t4 + (up ? 2 : 0) + (up2 ? 1 : 0)][c] = q;
+                if (part < 4) s_y[buf][t4 + (up ? 2 : 0) + (up2 ? 1 : 0)][c] = q;
               }
             }
           }
         }
       }
-      __syncthreads();
-      if (OUT && on) {
-        const Octet<T, WIDE> x = octet(0, px + t * p.x_row_stride);
-        Octet<T, WIDE> z;
-        if (pz) z = octet(2, pz + t * p.z_row_stride);
-        float o[8];
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          o[k] = fmaf(s_skip[o8 * 8 + k], x.get(k), s_y[tt][o8 * 8 + k]);
-          if (pz) o[k] *= gate_f(z.get(k));
-        }
-        T* dst = py + t * p.y_row_stride;
-        if constexpr (WIDE) {
-          store8(dst, o);
-        } else {
-#pragma unroll
-          for (int k = 0; k < 8; ++k)
-            if (k < left) dst[k] = from_f<T>(o[k]);
-        }
+  };
+  // One run over the piece.  Without producers a thread does both: it prepares the next tile before it
+  // runs this one, so that one barrier a tile is enough and the warps of a CTA need not go in step.
+  auto pass = [&](auto out_tag) {
+    constexpr bool OUT = decltype(out_tag)::value;
+    if constexpr (SPLIT) {
+      __syncthreads();                               // the first tile is there
+      for (int k = 0; k < tiles; ++k) {
+        run(out_tag, k);
+        __syncthreads();
       }
+    } else {
+      fetch(out_tag, 0);
+      fetch(out_tag, 1);
+      asm volatile("cp.async.wait_group 1;" ::: "memory");
+      if (tiles > 0) prepare(out_tag, 0);
+      __syncthreads();
+      for (int k = 0; k < tiles; ++k) {
+        fetch(out_tag, k + 2);
+        asm volatile("cp.async.wait_group 1;" ::: "memory");
+        if (k + 1 < tiles) prepare(out_tag, k + 1);
+        run(out_tag, k);
+        __syncthreads();
+        if (OUT) finish(k);
+      }
+      asm volatile("cp.async.wait_group 0;" ::: "memory");
     }
   };
 
-  float sum_s[CH] = {};
   if (R > 1) {
-    if (rank == 0) pass(std::true_type(), sum_s);    // the first piece knows its state
-    else if (rank < R - 1) pass(std::false_type(), sum_s);
+    if (rank == 0) pass(std::true_type());    // the first piece knows its state
+    else if (rank < R - 1) pass(std::false_type());
     cluster.sync();                                  // every CTA of the cluster has started: its shared memory is there
     // to every later piece (stores over the cluster need no answer; loads were ten times slower)
     for (int r = rank + 1; r < R; ++r) {
@@ -472,20 +562,20 @@ __global__ void __launch_bounds__(kThreads, CH == 2 ? 8 : 12) scan_kernel(const 
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
               u64& hh = h[j][2 * i + k];
-              const float2 x2 = unpack2(mul2(pack2(q, q), a[j][2 * i + k]));
-              const u64 decay = pack2(exp2_approx(x2.x), exp2_approx(x2.y));
+              const u64 decay = exp2_approx2(mul2(both(q), a[j][2 * i + k]));
               // the first piece's end state is whole already
               hh = r ? fma2(decay, hh, k ? end.y : end.x) : (k ? end.y : end.x);
             }
           }
         }
       }
-      pass(std::true_type(), sum_s);
+      pass(std::true_type());
     }
   } else {
-    pass(std::true_type(), sum_s);
+    pass(std::true_type());
   }
 
+  if (!SPLIT) zeros();
   if (rank == R - 1 && p.state_out) {
 #pragma unroll
     for (int j = 0; j < CH; ++j) {
@@ -501,11 +591,6 @@ __global__ void __launch_bounds__(kThreads, CH == 2 ? 8 : 12) scan_kernel(const 
       }
     }
   }
-  // frames behind the end are zero
-  for (int t = len + rank * TT + tt; t < p.t_max; t += R * TT)
-#pragma unroll
-    for (int k = 0; k < 8; ++k)
-      if (k < left) py[t * p.y_row_stride + k] = from_f<T>(0.f);
 }
 
 // A few frames: L lanes of 4 states to a channel, neighbouring lanes on neighbouring memory.
@@ -592,27 +677,30 @@ gam_status launch_step(const gam_scan_args& p, cudaStream_t s) {
 
 template <typename T, int S, int L, int CH>
 gam_status launch_scan(const gam_scan_args& p, int sms, cudaStream_t s) {
-  constexpr int CT = kThreads / L * CH, TT = kTile / CT;
+  using Shape = ScanShape<T, S, L, CH>;
+  constexpr int CT = Shape::CT, TT = Shape::TT;
   const int64_t ctas = (int64_t)((p.d + CT - 1) / CT) * p.batch;
-  // split while the pieces keep two tiles and the CTAs do not fill the SMs
-  int R = 1;
-  if (CH == 1)
-    while (R < 8 && ctas * R * 2 <= (int64_t)sms * 8 && p.t_max >= R * 2 * 2 * TT) R *= 2;
-  if (R == 2) R = 1;                                 // twice the work for twice the SMs gains nothing
-  if (ctas * R > INT32_MAX) return op_fail(GAM_ERR_CAPACITY, "batch * d too large for one call");
   constexpr int V = 16 / sizeof(T);
   const bool wide = p.d % 8 == 0 && aligned(p.x, 16) && aligned(p.dt, 16) && aligned(p.z, 16) && aligned(p.y, 16) &&
                     p.x_batch_stride % V == 0 && p.x_row_stride % V == 0 && p.dt_batch_stride % V == 0 &&
                     p.dt_row_stride % V == 0 && p.z_batch_stride % V == 0 && p.z_row_stride % V == 0 &&
                     p.y_batch_stride % V == 0 && p.y_row_stride % V == 0;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(ctas * R));
-  cfg.blockDim = dim3(kThreads);
-  cfg.stream = s;
   constexpr int PER = 4 / sizeof(T);
   const bool pair = aligned(p.b, 4) && aligned(p.c, 4) && p.b_batch_stride % PER == 0 && p.b_row_stride % PER == 0 &&
                     p.c_batch_stride % PER == 0 && p.c_row_stride % PER == 0;
-  cfg.dynamicSmemBytes = (pair ? 4 * TT * S * L * sizeof(T) : 0) + (wide ? 6 * kTile * sizeof(T) : 0) + (R - 1) * CT * (S * L + 1) * sizeof(float);
+  // split while the pieces keep two tiles and all CTAs are on the SMs at once (6 to an SM, or what shared memory allows)
+  int R = 1;
+  if (CH == 1)
+    while (R < 8 && p.t_max >= R * 2 * 2 * TT &&
+           ctas * R * 2 <= sms * std::min<int64_t>(6, 227 * 1024 / (Shape::bytes(wide, pair, R * 2) + CT * 8 + 1088)))
+      R *= 2;
+  if (R == 2) R = 1;                                 // twice the work for twice the SMs gains nothing
+  if (ctas * R > INT32_MAX) return op_fail(GAM_ERR_CAPACITY, "batch * d too large for one call");
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(ctas * R));
+  cfg.blockDim = dim3(Shape::THREADS);
+  cfg.stream = s;
+  cfg.dynamicSmemBytes = Shape::bytes(wide, pair, R);
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = R;
@@ -620,8 +708,7 @@ gam_status launch_scan(const gam_scan_args& p, int sms, cudaStream_t s) {
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   auto kernel = wide ? scan_kernel<T, S, L, CH, true> : scan_kernel<T, S, L, CH, false>;
-  constexpr int kFixed = kTile * 8 + TT * S * L * 8 + kTile * 4 + CT * 8 + 1024 + 64;  // static and reserved shared memory
-  if (cfg.dynamicSmemBytes + kFixed > 48 * 1024) {
+  if (cfg.dynamicSmemBytes + CT * 8 + 64 > 48 * 1024) {  // with the static part
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)cfg.dynamicSmemBytes);
     if (e != cudaSuccess) return launch_status(e);
   }
@@ -632,7 +719,7 @@ gam_status launch_scan(const gam_scan_args& p, int sms, cudaStream_t s) {
 // lanes with one channel of S1 states, and a cluster over the time axis.
 template <typename T, int S, int L, int S1, int L1>
 gam_status launch_pair(const gam_scan_args& p, int sms, cudaStream_t s) {
-  constexpr int CT = kThreads / L * 2;
+  constexpr int CT = kLanes / L * 2;
   const int64_t ctas = (int64_t)((p.d + CT - 1) / CT) * p.batch;
   return ctas >= 4 * sms ? launch_scan<T, S, L, 2>(p, sms, s) : launch_scan<T, S1, L1, 1>(p, sms, s);
 }
