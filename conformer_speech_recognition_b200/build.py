@@ -3,7 +3,9 @@
 Compiles every ``csrc/*.cu`` for sm_100a with nvcc (object files under
 ``_build/`` at the repository root, in parallel) and links them into
 ``conformer_speech_recognition_b200/libgam.so``.  nvcc cross-compiles, so this
-runs on a machine without a GPU.
+runs on a machine without a GPU.  ``csrc/python_ops.cpp`` (the marshalling of
+the streaming-block operators' Python calls) is compiled against torch's headers
+into ``conformer_speech_recognition_b200/_ops.so`` beside it.
 
     python -m conformer_speech_recognition_b200.build [--force] [-j N]
 """
@@ -11,16 +13,19 @@ from __future__ import annotations
 
 import argparse
 import concurrent.futures as cf
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libgam.so")
+OPS = os.path.join(PKG, "_ops.so")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
@@ -55,12 +60,32 @@ def _compile(src: str, force: bool, hdr_mtime: float, extra) -> str:
     return obj
 
 
+def _build_ops(force: bool) -> None:
+    src = os.path.join(CSRC, "python_ops.cpp")
+    newest = max(os.path.getmtime(src), os.path.getmtime(os.path.join(ROOT, "include", "gam.h")))
+    if not force and os.path.exists(OPS) and os.path.getmtime(OPS) >= newest:
+        return
+    torch = importlib.util.find_spec("torch").submodule_search_locations[0]
+    inc, lib = os.path.join(torch, "include"), os.path.join(torch, "lib")
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
+    cmd = [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+           "-I", inc, "-I", os.path.join(inc, "torch", "csrc", "api", "include"),
+           "-I", sysconfig.get_paths()["include"], "-isystem", os.path.join(cuda, "include"), src, "-o", OPS + ".tmp",
+           "-L", lib, "-Wl,-rpath," + lib, "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10_cuda", "-lc10"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed for {src}:\n{r.stdout}\n{r.stderr}")
+    os.replace(OPS + ".tmp", OPS)
+
+
 def build(force: bool = False, jobs: int = 8, verbose: bool = False, extra=()) -> str:
     os.makedirs(BUILD, exist_ok=True)
     srcs = _sources()
     hdr = _headers_mtime()
     with cf.ThreadPoolExecutor(max_workers=jobs) as ex:
+        ops = ex.submit(_build_ops, force)
         objs = list(ex.map(lambda s: _compile(s, force, hdr, list(extra)), srcs))
+        ops.result()
     newest = max(os.path.getmtime(o) for o in objs)
     if force or not os.path.exists(LIB) or os.path.getmtime(LIB) < newest:
         cmd = [nvcc(), *ARCH, "-shared", "-o", LIB, *objs, "-lcudart"]

@@ -9,13 +9,13 @@ from __future__ import annotations
 
 import ctypes
 import os
-import struct
 from typing import Dict, Optional, Tuple
 
 import numpy as np
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libgam.so")
+OPS_PATH = os.path.join(_HERE, "_ops.so")
 
 GAM_FP32, GAM_FP16, GAM_INT8_G64, GAM_INT6_G64, GAM_INT4_G64 = 0, 1, 2, 3, 4
 PRECISION = {"fp32": GAM_FP32, "fp16": GAM_FP16, "int8_g64": GAM_INT8_G64, "int6_g64": GAM_INT6_G64,
@@ -27,8 +27,6 @@ NORM = {"none": 0, "layer": 1, "rms": 2}
 
 STATUS = {0: "GAM_OK", 1: "GAM_ERR_INVALID_ARG", 2: "GAM_ERR_SHAPE", 3: "GAM_ERR_CAPACITY", 4: "GAM_ERR_WEIGHTS",
           5: "GAM_ERR_UNSUPPORTED_DEVICE", 6: "GAM_ERR_CUDA", 7: "GAM_ERR_DEVICE_TIMEOUT"}
-
-GROUP = 64  # weights per scale of the quantised modes
 
 # Every entry point declared in include/gam.h.
 EXPORTS = ("gam_status_string", "gam_last_error", "gam_plan_lengths", "gam_create", "gam_destroy", "gam_logmel",
@@ -424,46 +422,25 @@ def gam_ctc_collapse_noalloc(logits, lengths_dev, tokens, counts, stream=None):
 
 
 # ---- streaming-block operators ----
-# Host tuples of the argument structs in gam.h, laid out by struct.pack.
-_SCAN_ARGS = struct.Struct("12Q12q6i")       # gam_scan_args
-_NORM_ARGS = struct.Struct("10Q7q6i2f")      # gam_residual_norm_args
+# Their tensors are checked and passed on by the extension module _ops (csrc/python_ops.cpp).
+
+_ops_module = None
 
 
-def _op_dtype(t, name: str) -> int:
-    import torch
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise GamError(1, f"{name} must be a CUDA tensor")
-    code = {torch.float32: DTYPE_F32, torch.float16: DTYPE_F16, torch.bfloat16: DTYPE_BF16}.get(t.dtype)
-    if code is None:
-        raise GamError(1, f"{name} must be float32, float16 or bfloat16, got {t.dtype}")
-    return code
-
-
-def _op_arg(t, name: str, shape, dtype, dev: int, packed: bool = False) -> int:
-    """Address of a CUDA tensor of this shape and type on device `dev` whose last
-    dimension is contiguous (`packed`: all of it); 0 for None."""
-    if t is None:
-        return 0
-    if not getattr(t, "is_cuda", False):
-        raise GamError(1, f"{name} must be a CUDA tensor")
-    if t.dtype != dtype:
-        raise GamError(1, f"{name} must be {dtype}, got {t.dtype}")
-    if t.get_device() != dev:
-        raise GamError(1, f"{name} is on cuda:{t.get_device()}, expected cuda:{dev}")
-    if tuple(t.shape) != shape:
-        raise GamError(1, f"{name} must have shape {list(shape)}, got {list(t.shape)}")
-    if packed:
-        if not t.is_contiguous():
-            raise GamError(1, f"{name} must be contiguous")
-    elif shape[-1] > 1 and t.stride(-1) != 1:
-        raise GamError(1, f"the last dimension of {name} must be contiguous")
-    return t.data_ptr()
-
-
-def _op_need(**tensors):
-    for name, t in tensors.items():
-        if not getattr(t, "is_cuda", False):
-            raise GamError(1, f"{name} must be a CUDA tensor")
+def _ops():
+    """The marshalling module, bound to libgam.so's entry points (raises if it was not built)."""
+    global _ops_module
+    if _ops_module is None:
+        import torch  # noqa: F401  (its libraries, which _ops links against)
+        if not os.path.exists(OPS_PATH):
+            raise RuntimeError(f"{OPS_PATH} is missing: build it with "
+                               "`python -m conformer_speech_recognition_b200.build`")
+        from . import _ops as module
+        L = lib()
+        entries = (L.gam_last_error, L.gam_quant_linear, L.gam_short_conv, L.gam_selective_scan, L.gam_residual_norm)
+        module.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in entries), GamError)
+        _ops_module = module
+    return _ops_module
 
 
 def _op_code(table: Dict[str, int], key, name: str) -> int:
@@ -472,35 +449,8 @@ def _op_code(table: Dict[str, int], key, name: str) -> int:
     return table[key]
 
 
-class _OpStream:
-    """The device and stream of one operator call: `raw` is the cudaStream_t,
-    `empty` allocates outputs that belong to that stream."""
-
-    def __init__(self, t, stream):
-        import torch
-        self.dev = t.get_device()
-        self.guard = torch.cuda.device(self.dev) if torch.cuda.current_device() != self.dev else None
-        if stream is None:
-            self.stream = None
-            self.raw = torch._C._cuda_getCurrentRawStream(self.dev)
-        else:
-            self.raw = _stream(stream)
-            self.stream = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(self.raw,
-                                                                                                         self.dev)
-
-    def empty(self, shape, dtype):
-        import torch
-        if self.stream is None:
-            return torch.empty(shape, dtype=dtype, device=self.dev)
-        with torch.cuda.stream(self.stream):
-            return torch.empty(shape, dtype=dtype, device=self.dev)
-
-    def call(self, fn, *args):
-        if self.guard is None:
-            _check(fn(*args, self.raw))
-        else:
-            with self.guard:
-                _check(fn(*args, self.raw))
+def _op_stream(stream) -> Optional[int]:
+    return None if stream is None else _stream(stream)
 
 
 def gam_quant_linear_pack(q) -> np.ndarray:
@@ -521,25 +471,8 @@ def gam_quant_linear(x, packed, scale, bias=None, act: str = "none", out=None, s
     uint8 [n, k / 2] (gam_quant_linear_pack); scale: CUDA float16 [n, k / 64];
     bias: CUDA float32 [n] or None; act: "none" or "swish".  Returns out [rows, n]
     in x's type."""
-    import torch
-    code = _op_dtype(x, "x")
-    if x.ndim != 2 or getattr(packed, "ndim", 0) != 2:
-        raise GamError(1, "x must be [rows, k] and packed [n, k / 2]")
-    _op_need(packed=packed, scale=scale)
-    rows, k = x.shape
-    n = packed.shape[0]
-    on = _OpStream(x, stream)
-    if out is None:
-        out = on.empty((rows, n), x.dtype)
-    dev = on.dev
-    if k % GROUP:
-        raise GamError(2, f"k must be a multiple of {GROUP}")
-    on.call(lib().gam_quant_linear, _op_arg(x, "x", (rows, k), x.dtype, dev), code, x.stride(0),
-            _op_arg(packed, "packed", (n, k // 2), torch.uint8, dev, True),
-            _op_arg(scale, "scale", (n, k // GROUP), torch.float16, dev, True),
-            _op_arg(bias, "bias", (n,), torch.float32, dev, True), _op_code(ACT, act, "act"), rows, n, k,
-            _op_arg(out, "out", (rows, n), x.dtype, dev), out.stride(0))
-    return out
+    return (_ops_module or _ops()).quant_linear(x, packed, scale, bias, _op_code(ACT, act, "act"), out,
+                                                _op_stream(stream))
 
 
 def gam_short_conv(x, weight, bias=None, act: str = "swish", lengths=None, state=None, out=None, state_out=None,
@@ -549,28 +482,8 @@ def gam_short_conv(x, weight, bias=None, act: str = "swish", lengths=None, state
     state: the taps - 1 inputs before frame 0, [batch, taps - 1, d] in x's type
     (None: zeros); lengths: CUDA int32 [batch] (None: all t frames).  Returns
     (out [batch, t, d], state_out [batch, taps - 1, d]); state_out may be state."""
-    import torch
-    code = _op_dtype(x, "x")
-    if x.ndim != 3 or getattr(weight, "ndim", 0) != 2:
-        raise GamError(1, "x must be [batch, t, d] and weight [d, taps]")
-    _op_need(weight=weight)
-    batch, t, d = x.shape
-    taps = weight.shape[1]
-    on = _OpStream(x, stream)
-    dev, dtype = on.dev, x.dtype
-    sshape = (batch, max(taps - 1, 0), d)
-    if out is None:
-        out = on.empty((batch, t, d), dtype)
-    if state_out is None:
-        state_out = on.empty(sshape, dtype)
-    on.call(lib().gam_short_conv, _op_arg(x, "x", (batch, t, d), dtype, dev), code, x.stride(0), x.stride(1),
-            _op_arg(weight, "weight", (d, taps), torch.float32, dev, True),
-            _op_arg(bias, "bias", (d,), torch.float32, dev, True), taps, _op_code(ACT, act, "act"), batch, t, d,
-            _op_arg(lengths, "lengths", (batch,), torch.int32, dev, True),
-            _op_arg(state, "state", sshape, dtype, dev, True),
-            _op_arg(state_out, "state_out", sshape, dtype, dev, True),
-            _op_arg(out, "out", (batch, t, d), dtype, dev), out.stride(0), out.stride(1))
-    return out, state_out
+    return (_ops_module or _ops()).short_conv(x, weight, bias, _op_code(ACT, act, "act"), lengths, state, out,
+                                              state_out, _op_stream(stream))
 
 
 def gam_selective_scan(x, dt, a, b, c, d_skip=None, z=None, dt_bias=None, dt_softplus: bool = True, lengths=None,
@@ -580,32 +493,8 @@ def gam_selective_scan(x, dt, a, b, c, d_skip=None, z=None, dt_bias=None, dt_sof
 
     x, dt, b, c, z share one type; a, d_skip, dt_bias and the states are float32.
     Returns (out [batch, t, d], state_out [batch, d, n]); state_out may be state."""
-    import torch
-    code = _op_dtype(x, "x")
-    if x.ndim != 3 or getattr(a, "ndim", 0) != 2:
-        raise GamError(1, "x must be [batch, t, d] and a [d, n]")
-    _op_need(dt=dt, a=a, b=b, c=c)
-    shape = batch, t, d = tuple(x.shape)
-    n = a.shape[1]
-    on = _OpStream(x, stream)
-    dev, dtype, f32 = on.dev, x.dtype, torch.float32
-    if out is None:
-        out = on.empty(shape, dtype)
-    if state_out is None:
-        state_out = on.empty((batch, d, n), f32)
-    strides = [s for v in (x, dt, b, c) for s in v.stride()[:2]]
-    args = _SCAN_ARGS.pack(
-        _op_arg(x, "x", shape, dtype, dev), _op_arg(dt, "dt", shape, dtype, dev),
-        _op_arg(a, "a", (d, n), f32, dev, True), _op_arg(b, "b", (batch, t, n), dtype, dev),
-        _op_arg(c, "c", (batch, t, n), dtype, dev), _op_arg(d_skip, "d_skip", (d,), f32, dev, True),
-        _op_arg(z, "z", shape, dtype, dev), _op_arg(dt_bias, "dt_bias", (d,), f32, dev, True),
-        _op_arg(lengths, "lengths", (batch,), torch.int32, dev, True),
-        _op_arg(state, "state", (batch, d, n), f32, dev, True),
-        _op_arg(state_out, "state_out", (batch, d, n), f32, dev, True), _op_arg(out, "out", shape, dtype, dev),
-        *strides, *(z.stride()[:2] if z is not None else (0, 0)), *out.stride()[:2],
-        code, batch, t, d, n, 1 if dt_softplus else 0)
-    on.call(lib().gam_selective_scan, args)
-    return out, state_out
+    return (_ops_module or _ops()).selective_scan(x, dt, a, b, c, d_skip, z, dt_bias, dt_softplus, lengths, state, out,
+                                                  state_out, _op_stream(stream))
 
 
 def gam_residual_norm(x, y, alpha: float = 1.0, layer_scale=None, gate=None, gate_act: str = "none",
@@ -617,31 +506,9 @@ def gam_residual_norm(x, y, alpha: float = 1.0, layer_scale=None, gate=None, gat
     serving rows / gate_rows consecutive rows; weights, biases and layer_scale are
     float32 [d].  Returns (x_out in x's type, out in y's type); x_out may be x and
     out may be y."""
-    import torch
-    xcode, code = _op_dtype(x, "x"), _op_dtype(y, "y")
-    if x.ndim != 2:
-        raise GamError(1, "x must be [rows, d]")
-    shape = rows, d = tuple(x.shape)
-    on = _OpStream(x, stream)
-    dev, f32 = on.dev, torch.float32
-    if x_out is None:
-        x_out = on.empty(shape, x.dtype)
-    if out is None:
-        out = on.empty(shape, y.dtype)
-    if gate is not None and getattr(gate, "ndim", 0) != 2:
-        raise GamError(1, "gate must be [gate_rows, d]")
-    vec = [_op_arg(t, name, (d,), f32, dev, True)
-           for t, name in ((layer_scale, "layer_scale"), (post_weight, "post_weight"), (post_bias, "post_bias"),
-                           (pre_weight, "pre_weight"), (pre_bias, "pre_bias"))]
-    args = _NORM_ARGS.pack(
-        _op_arg(x, "x", shape, x.dtype, dev), _op_arg(y, "y", shape, y.dtype, dev),
-        _op_arg(gate, "gate", (gate.shape[0], d), y.dtype, dev) if gate is not None else 0, *vec,
-        _op_arg(x_out, "x_out", shape, x.dtype, dev), _op_arg(out, "out", shape, y.dtype, dev),
-        x.stride(0), y.stride(0), gate.stride(0) if gate is not None else 0, x_out.stride(0), out.stride(0),
-        rows, gate.shape[0] if gate is not None else 1, xcode, code, d, _op_code(ACT, gate_act, "gate_act"),
-        _op_code(NORM, post, "post"), _op_code(NORM, pre, "pre"), alpha, eps)
-    on.call(lib().gam_residual_norm, args)
-    return x_out, out
+    return (_ops_module or _ops()).residual_norm(
+        x, y, alpha, layer_scale, gate, _op_code(ACT, gate_act, "gate_act"), _op_code(NORM, post, "post"), post_weight,
+        post_bias, _op_code(NORM, pre, "pre"), pre_weight, pre_bias, eps, x_out, out, _op_stream(stream))
 
 
 def gam_rnnt_attach(ctx: Context, rnnt_cfg: dict, weights: Dict[str, np.ndarray]):

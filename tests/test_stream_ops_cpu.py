@@ -163,23 +163,6 @@ def test_binding_refuses_cpu_tensors(L):
         assert e.value.name == "GAM_ERR_INVALID_ARG"
 
 
-def test_argument_structs_have_the_headers_size(tmp_path, L):
-    import os
-    import shutil
-    import subprocess
-    from conftest import ROOT
-    cc = shutil.which("gcc")
-    if cc is None:
-        pytest.skip("no C compiler")
-    src = tmp_path / "sizes.c"
-    src.write_text('#include "gam.h"\n#include <stdio.h>\nint main(void){printf("%zu %zu", sizeof(gam_scan_args), '
-                   'sizeof(gam_residual_norm_args));return 0;}\n')
-    exe = str(tmp_path / "sizes")
-    subprocess.run([cc, "-I", os.path.join(ROOT, "include"), str(src), "-o", exe], check=True)
-    got = subprocess.run([exe], capture_output=True, text=True, check=True).stdout.split()
-    assert [int(v) for v in got] == [gam._SCAN_ARGS.size, gam._NORM_ARGS.size]
-
-
 # ---- oracle pins ---------------------------------------------------------------
 
 def test_oracle_conv_is_a_causal_correlation():
