@@ -2,9 +2,10 @@
 //
 //   x' = x + alpha * layer_scale * gate_act(gate) * post_norm(y),  u = pre_norm(x')
 //
-// One pass: a group of G threads (a warp, or a CTA for wide rows) holds a row of
-// y and x in registers, so each is read once; statistics are two-pass in fp32
-// (mean, then the centred squares) over those registers.
+// One pass: a group of G threads (a warp, or a CTA for wide or few rows) holds a
+// row of y and x in registers, so each is read once; all loads of a row are on
+// their way before the first is used.  Statistics are two-pass in fp32 (mean,
+// then the centred squares) over those registers.  The bound is memory.
 #include "stream_ops.cuh"
 
 namespace gam {
@@ -30,113 +31,125 @@ __device__ __forceinline__ float row_sum(float v, float (*red)[32], int& turn) {
   return v;
 }
 
+// Row position of a thread: it holds accesses j G + tid of V columns, j < NV.  Accesses
+// past the row's end load the last one again and count nothing.
+struct Place {
+  int tid, G, vecs, d;
+  __device__ __forceinline__ bool on(int j) const { return j * G + tid < vecs; }
+  template <int V>
+  __device__ __forceinline__ int col(int j) const { return min(j * G + tid, vecs - 1) * V; }
+};
+
 template <int V>
 __device__ __forceinline__ void load_param(const float* p, int c, float fill, float (&out)[V]) {
+  if constexpr (V == 1) {
+    out[0] = p ? __ldg(p + c) : fill;
+  } else {  // 16-byte aligned with the rows
 #pragma unroll
-  for (int i = 0; i < V; ++i) out[i] = p ? __ldg(p + c + i) : fill;
+    for (int i = 0; i < V / 4; ++i) {
+      const float4 q = p ? __ldg(reinterpret_cast<const float4*>(p + c) + i) : make_float4(fill, fill, fill, fill);
+      out[4 * i] = q.x, out[4 * i + 1] = q.y, out[4 * i + 2] = q.z, out[4 * i + 3] = q.w;
+    }
+  }
 }
 
-// v <- norm(v) over the row; thread tid of G holds columns (j G + tid) V + i
+// v <- norm(v) over the row
 template <bool WARP, int V, int NV>
-__device__ __forceinline__ void norm_row(float (&v)[NV][V], int kind, const float* w, const float* b, float eps, int d,
-                                         int tid, int G, float (*red)[32], int& turn) {
+__device__ __forceinline__ void norm_row(float (&v)[NV][V], int kind, const float* w, const float* b, float eps,
+                                         const Place& at, float (*red)[32], int& turn) {
+  // one access a thread: its weights come while the row is summed
+  float w0[V], b0[V];
+  if constexpr (NV == 1) {
+    load_param<V>(w, at.col<V>(0), 1.f, w0);
+    load_param<V>(kind == GAM_NORM_LAYER ? b : nullptr, at.col<V>(0), 0.f, b0);
+  }
+  const float inv = 1.f / at.d;
   if (kind == GAM_NORM_LAYER) {
     float s = 0.f;
 #pragma unroll
     for (int j = 0; j < NV; ++j)
 #pragma unroll
       for (int i = 0; i < V; ++i) s += v[j][i];
-    const float mean = row_sum<WARP>(s, red, turn) / d;
+    const float mean = row_sum<WARP>(s, red, turn) * inv;
 #pragma unroll
     for (int j = 0; j < NV; ++j)
 #pragma unroll
-      for (int i = 0; i < V; ++i) v[j][i] = (j * G + tid) * V < d ? v[j][i] - mean : 0.f;
+      for (int i = 0; i < V; ++i) v[j][i] = at.on(j) ? v[j][i] - mean : 0.f;
   }
   float q = 0.f;
 #pragma unroll
   for (int j = 0; j < NV; ++j)
 #pragma unroll
     for (int i = 0; i < V; ++i) q = fmaf(v[j][i], v[j][i], q);
-  const float r = rsqrtf(row_sum<WARP>(q, red, turn) / d + eps);
+  const float r = rsqrtf(fmaf(row_sum<WARP>(q, red, turn), inv, eps));
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
-    const int c = (j * G + tid) * V;
-    if (c < d) {
-      float ww[V], bb[V];
-      load_param<V>(w, c, 1.f, ww);
-      load_param<V>(kind == GAM_NORM_LAYER ? b : nullptr, c, 0.f, bb);
-#pragma unroll
-      for (int i = 0; i < V; ++i) v[j][i] = fmaf(v[j][i] * r, ww[i], bb[i]);
+    if constexpr (NV > 1) {
+      load_param<V>(w, at.col<V>(j), 1.f, w0);
+      load_param<V>(kind == GAM_NORM_LAYER ? b : nullptr, at.col<V>(j), 0.f, b0);
     }
+#pragma unroll
+    for (int i = 0; i < V; ++i) v[j][i] = at.on(j) ? fmaf(v[j][i] * r, w0[i], b0[i]) : 0.f;
   }
 }
 
 template <typename TX, typename TY, bool WARP, int V, int NV>
-__global__ void __launch_bounds__(WARP ? 128 : V == 8 ? 512 : 1024) residual_norm_kernel(const gam_residual_norm_args p, int64_t per_gate) {
+__global__ void __launch_bounds__(WARP ? 128 : V == 8 ? 512 : 1024)
+residual_norm_kernel(const gam_residual_norm_args p, const int64_t per_gate) {
   __shared__ float red[2][32];
-  const int G = WARP ? 32 : blockDim.x;
-  const int tid = WARP ? threadIdx.x & 31 : threadIdx.x;
   const int64_t row = WARP ? (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5) : (int64_t)blockIdx.x;
   if (row >= p.rows) return;
-  const int d = p.d;
-  int turn = 0;
-  float x[NV][V], y[NV][V];
+  const Place at{(int)(WARP ? threadIdx.x & 31 : threadIdx.x), (int)(WARP ? 32 : blockDim.x), (p.d + V - 1) / V, p.d};
   const TX* xr = (const TX*)p.x + row * p.x_stride;
   const TY* yr = (const TY*)p.y + row * p.y_stride;
-#pragma unroll
-  for (int j = 0; j < NV; ++j) {
-    const int c = (j * G + tid) * V;
-    if (c < d) {
-      const Vec<TX, V> a = *reinterpret_cast<const Vec<TX, V>*>(xr + c);
-      const Vec<TY, V> b = *reinterpret_cast<const Vec<TY, V>*>(yr + c);
-#pragma unroll
-      for (int i = 0; i < V; ++i) x[j][i] = to_f(a.v[i]), y[j][i] = to_f(b.v[i]);
-    } else {
-#pragma unroll
-      for (int i = 0; i < V; ++i) x[j][i] = y[j][i] = 0.f;
-    }
-  }
-  if (p.post_norm) norm_row<WARP, V, NV>(y, p.post_norm, p.post_weight, p.post_bias, p.eps, d, tid, G, red, turn);
   const TY* gr = p.gate ? (const TY*)p.gate + row / per_gate * p.gate_stride : nullptr;
+  Raw<TX, V> rx[NV];
+  Raw<TY, V> ry[NV], rg[NV];
+#pragma unroll
+  for (int j = 0; j < NV; ++j) ry[j].load(yr + at.col<V>(j));
+#pragma unroll
+  for (int j = 0; j < NV; ++j) rx[j].load(xr + at.col<V>(j));
+  if (gr)
+#pragma unroll
+    for (int j = 0; j < NV; ++j) rg[j].load(gr + at.col<V>(j));
+  int turn = 0;
+  float y[NV][V], x[NV][V];
+#pragma unroll
+  for (int j = 0; j < NV; ++j)
+#pragma unroll
+    for (int i = 0; i < V; ++i) y[j][i] = at.on(j) ? ry[j].get(i) : 0.f;
+  if (p.post_norm) norm_row<WARP, V, NV>(y, p.post_norm, p.post_weight, p.post_bias, p.eps, at, red, turn);
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
-    const int c = (j * G + tid) * V;
-    if (c < d) {
-      if (gr) {
-        const Vec<TY, V> g = *reinterpret_cast<const Vec<TY, V>*>(gr + c);
+    float ls[V];
+    load_param<V>(p.layer_scale, at.col<V>(j), 1.f, ls);
 #pragma unroll
-        for (int i = 0; i < V; ++i) y[j][i] *= activate(to_f(g.v[i]), p.gate_act);
-      }
-      float ls[V];
-      load_param<V>(p.layer_scale, c, 1.f, ls);
-#pragma unroll
-      for (int i = 0; i < V; ++i) x[j][i] = fmaf(p.alpha * ls[i], y[j][i], x[j][i]);
-      if (p.x_out) {
-        Vec<TX, V> o;
-#pragma unroll
-        for (int i = 0; i < V; ++i) o.v[i] = from_f<TX>(x[j][i]);
-        *reinterpret_cast<Vec<TX, V>*>((TX*)p.x_out + row * p.x_out_stride + c) = o;
-      }
+    for (int i = 0; i < V; ++i) {
+      if (gr) y[j][i] *= activate(rg[j].get(i), p.gate_act);
+      x[j][i] = at.on(j) ? fmaf(p.alpha * ls[i], y[j][i], rx[j].get(i)) : 0.f;
+    }
+    if (p.x_out && at.on(j)) {
+      Raw<TX, V> o;
+      o.set(x[j]);
+      o.store((TX*)p.x_out + row * p.x_out_stride + at.col<V>(j));
     }
   }
   if (!p.u) return;
-  if (p.pre_norm) norm_row<WARP, V, NV>(x, p.pre_norm, p.pre_weight, p.pre_bias, p.eps, d, tid, G, red, turn);
+  if (p.pre_norm) norm_row<WARP, V, NV>(x, p.pre_norm, p.pre_weight, p.pre_bias, p.eps, at, red, turn);
 #pragma unroll
-  for (int j = 0; j < NV; ++j) {
-    const int c = (j * G + tid) * V;
-    if (c < d) {
-      Vec<TY, V> o;
-#pragma unroll
-      for (int i = 0; i < V; ++i) o.v[i] = from_f<TY>(x[j][i]);
-      *reinterpret_cast<Vec<TY, V>*>((TY*)p.u + row * p.u_stride + c) = o;
+  for (int j = 0; j < NV; ++j)
+    if (at.on(j)) {
+      Raw<TY, V> o;
+      o.set(x[j]);
+      o.store((TY*)p.u + row * p.u_stride + at.col<V>(j));
     }
-  }
 }
 
 template <typename TX, typename TY, int V>
-gam_status launch_v(const gam_residual_norm_args& p, int64_t per_gate, cudaStream_t s) {
+gam_status launch_v(const gam_residual_norm_args& p, int64_t per_gate, int sms, cudaStream_t s) {
   const int vecs = (p.d + V - 1) / V;
-  if (vecs <= 128) {  // a warp holds a row: up to 4 accesses per lane
+  // rows enough for 8 warps to an SM: a warp holds a row, up to 4 accesses to a lane
+  if (vecs <= 128 && (p.rows >= 8 * sms || vecs <= 32)) {
     const int64_t grid = (p.rows + 3) / 4;
     if (grid > INT32_MAX) return op_fail(GAM_ERR_CAPACITY, "too many rows for one call");
     if (vecs <= 32) residual_norm_kernel<TX, TY, true, V, 1><<<(unsigned)grid, 128, 0, s>>>(p, per_gate);
@@ -147,19 +160,25 @@ gam_status launch_v(const gam_residual_norm_args& p, int64_t per_gate, cudaStrea
   if (p.rows > INT32_MAX) return op_fail(GAM_ERR_CAPACITY, "too many rows for one call");
   const unsigned grid = (unsigned)p.rows;
   auto threads = [&](int nv) { return ((vecs + nv - 1) / nv + 31) / 32 * 32; };
-  if (vecs <= 1024) residual_norm_kernel<TX, TY, false, V, 2><<<grid, threads(2), 0, s>>>(p, per_gate);
-  else if (vecs <= 4096) residual_norm_kernel<TX, TY, false, V, 4><<<grid, threads(4), 0, s>>>(p, per_gate);
-  else if constexpr (V == 1) residual_norm_kernel<TX, TY, false, V, 16><<<grid, threads(16), 0, s>>>(p, per_gate);
+  if (vecs <= 512) residual_norm_kernel<TX, TY, false, V, 1><<<grid, threads(1), 0, s>>>(p, per_gate);
+  else if (vecs <= 1024) residual_norm_kernel<TX, TY, false, V, 2><<<grid, threads(2), 0, s>>>(p, per_gate);
+  else if (vecs <= 2048) residual_norm_kernel<TX, TY, false, V, 4><<<grid, threads(4), 0, s>>>(p, per_gate);
+  else if constexpr (V < 8) {
+    if (vecs <= 4096) residual_norm_kernel<TX, TY, false, V, V == 1 ? 8 : 4><<<grid, threads(V == 1 ? 8 : 4), 0, s>>>(p, per_gate);
+    else if constexpr (V == 1) residual_norm_kernel<TX, TY, false, V, 16><<<grid, threads(16), 0, s>>>(p, per_gate);
+  }
   return launch_status(cudaGetLastError());
 }
 
 template <typename TX, typename TY>
-gam_status launch(const gam_residual_norm_args& p, int64_t per_gate, cudaStream_t s) {
+gam_status launch(const gam_residual_norm_args& p, int64_t per_gate, int sms, cudaStream_t s) {
   constexpr int V = 16 / sizeof(TY);
   const bool wide = p.d % V == 0 && aligned(p.x, 16) && aligned(p.y, 16) && aligned(p.gate, 16) &&
                     aligned(p.x_out, 16) && aligned(p.u, 16) && p.x_stride % V == 0 && p.y_stride % V == 0 &&
-                    p.gate_stride % V == 0 && p.x_out_stride % V == 0 && p.u_stride % V == 0;
-  return wide ? launch_v<TX, TY, V>(p, per_gate, s) : launch_v<TX, TY, 1>(p, per_gate, s);
+                    p.gate_stride % V == 0 && p.x_out_stride % V == 0 && p.u_stride % V == 0 &&
+                    aligned(p.layer_scale, 16) && aligned(p.post_weight, 16) && aligned(p.post_bias, 16) &&
+                    aligned(p.pre_weight, 16) && aligned(p.pre_bias, 16);
+  return wide ? launch_v<TX, TY, V>(p, per_gate, sms, s) : launch_v<TX, TY, 1>(p, per_gate, sms, s);
 }
 
 bool norm_kind(int k) { return k == GAM_NORM_NONE || k == GAM_NORM_LAYER || k == GAM_NORM_RMS; }
@@ -208,11 +227,11 @@ extern "C" gam_status gam_residual_norm(const gam_residual_norm_args* args, void
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const int64_t per_gate = p.rows / p.gate_rows;
     if (p.x_dtype == GAM_DTYPE_F32) {
-      if (p.dtype == GAM_DTYPE_F32) return launch<float, float>(p, per_gate, s);
-      if (p.dtype == GAM_DTYPE_F16) return launch<float, __half>(p, per_gate, s);
-      return launch<float, bf16>(p, per_gate, s);
+      if (p.dtype == GAM_DTYPE_F32) return launch<float, float>(p, per_gate, sms, s);
+      if (p.dtype == GAM_DTYPE_F16) return launch<float, __half>(p, per_gate, sms, s);
+      return launch<float, bf16>(p, per_gate, sms, s);
     }
-    if (p.dtype == GAM_DTYPE_F16) return launch<__half, __half>(p, per_gate, s);
-    return launch<bf16, bf16>(p, per_gate, s);
+    if (p.dtype == GAM_DTYPE_F16) return launch<__half, __half>(p, per_gate, sms, s);
+    return launch<bf16, bf16>(p, per_gate, sms, s);
   });
 }

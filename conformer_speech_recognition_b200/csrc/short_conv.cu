@@ -4,7 +4,10 @@
 //
 // A thread owns V channels (one 16-byte access; one channel when the rows are
 // not 16-byte aligned) and a segment of the time axis.  It keeps the last
-// taps - 1 rows in registers, so inside a segment every input is read once.
+// taps - 1 rows in registers, so inside a segment every input is read once, and
+// has R rows on their way at a time (the bound is memory).
+#include <algorithm>
+
 #include "stream_ops.cuh"
 
 namespace gam {
@@ -20,124 +23,136 @@ struct ConvArgs {
   void* state_out;
   void* y;
   int64_t xb, xr, yb, yr;
-  int act, t_max, d, seg, segs, cblocks;
+  int act, batch, t_max, d, seg, segs, vecs;
 };
 
 constexpr int kThreads = 128;
 
-template <typename T, int V, int TAPS>
+template <typename T, int V, int TAPS, int R>
 __global__ void __launch_bounds__(kThreads) short_conv_kernel(const ConvArgs p) {
-  using Vt = Vec<T, V>;
+  using Row = Raw<T, V>;
   constexpr int H = TAPS - 1;                  // rows of history
-  constexpr int R = TAPS <= 5 ? 8 : 4;         // rows loaded ahead of their use
-  const int cb = blockIdx.x % p.cblocks;
-  const int rest = blockIdx.x / p.cblocks;
-  const int seg = rest % p.segs, b = rest / p.segs;
-  const int c = (cb * kThreads + threadIdx.x) * V;
-  if (c >= p.d) return;
+  const int64_t id = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+  const int64_t item = id / p.vecs;
+  if (item >= (int64_t)p.batch * p.segs) return;
+  const int c = (int)(id - item * p.vecs) * V;
+  const int seg = (int)(item % p.segs), b = (int)(item / p.segs);
   const int len = p.lengths ? min(max(p.lengths[b], 0), p.t_max) : p.t_max;
   const T* x = (const T*)p.x + b * p.xb + c;
   T* y = (T*)p.y + b * p.yb + c;
-  const T* sin = p.state_in ? (const T*)p.state_in + (int64_t)b * H * p.d + c : nullptr;
-  // row r of the input, r >= -H: the state's before 0
-  auto row = [&](int r) -> Vt {
-    if (r >= 0) return *reinterpret_cast<const Vt*>(x + r * p.xr);
-    if (sin) return *reinterpret_cast<const Vt*>(sin + (int64_t)(r + H) * p.d);
-    Vt z;
-#pragma unroll
-    for (int i = 0; i < V; ++i) z.v[i] = from_f<T>(0.f);
-    return z;
+  const T* past = p.state_in ? (const T*)p.state_in + (int64_t)b * H * p.d + c : nullptr;
+  // row r >= -H of the input: the state's before 0
+  auto row = [&](int r) {
+    Row v;
+    v.zero();
+    if (r >= 0) v.load(x + r * p.xr);
+    else if (past) v.load(past + (int64_t)(r + H) * p.d);
+    return v;
   };
-  const int t0 = seg * p.seg, t1 = min(t0 + p.seg, p.t_max);
-  float h[H][V];
+  const int t0 = seg * p.seg, t1 = min(t0 + p.seg, p.t_max), tv = min(t1, len);
+  Row in[R], h[H];
+  const bool work = t0 < tv;
+  if (work) {
 #pragma unroll
-  for (int j = 0; j < H; ++j) {
-    Vt r;
-    if (t0 < len) r = row(t0 - H + j);  // a segment behind the length reads nothing
+    for (int r = 0; r < R; ++r) in[r].load(x + min(t0 + r, tv - 1) * p.xr);  // repeats beyond the end are not used
 #pragma unroll
-    for (int i = 0; i < V; ++i) h[j][i] = t0 < len ? to_f(r.v[i]) : 0.f;
+    for (int j = 0; j < H; ++j) h[j] = row(t0 - H + j);
   }
   if (seg == 0 && p.state_out) {
-    // this thread alone touches its channels' state: all of it is read first, so
-    // state_out may be state_in
-    Vt keep[H];
+    // this thread alone touches its channels' state, and has read all of it: state_out may be state_in
+    Row keep[H];
 #pragma unroll
     for (int j = 0; j < H; ++j) keep[j] = row(len - H + j);
     T* so = (T*)p.state_out + (int64_t)b * H * p.d + c;
 #pragma unroll
-    for (int j = 0; j < H; ++j) *reinterpret_cast<Vt*>(so + (int64_t)j * p.d) = keep[j];
+    for (int j = 0; j < H; ++j) keep[j].store(so + (int64_t)j * p.d);
   }
-  float w[TAPS][V], bias[V];
+  if (work) {
+    float w[V * TAPS], bias[V];                // w[i TAPS + j]: channel i, tap j
+    const float* pw = p.w + (int64_t)c * TAPS;
+    if constexpr (V > 1) {                     // 16-byte aligned with the rows
 #pragma unroll
-  for (int i = 0; i < V; ++i) {
-    bias[i] = p.bias ? __ldg(p.bias + c + i) : 0.f;
-#pragma unroll
-    for (int j = 0; j < TAPS; ++j) w[j][i] = __ldg(p.w + (int64_t)(c + i) * TAPS + j);
-  }
-  for (int t = t0; t < t1; t += R) {
-    Vt in[R];
-#pragma unroll
-    for (int r = 0; r < R; ++r)
-      if (t + r < min(t1, len)) in[r] = row(t + r);
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-      if (t + r >= t1) break;
-      Vt out;
-      if (t + r < len) {
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-          const float cur = to_f(in[r].v[i]);
-          float acc = bias[i];
-#pragma unroll
-          for (int j = 0; j < H; ++j) acc = fmaf(w[j][i], h[j][i], acc);
-          acc = fmaf(w[H][i], cur, acc);
-#pragma unroll
-          for (int j = 0; j + 1 < H; ++j) h[j][i] = h[j + 1][i];
-          h[H - 1][i] = cur;
-          out.v[i] = from_f<T>(p.act == GAM_ACT_SWISH ? swish_f(acc) : acc);
-        }
-      } else {
-#pragma unroll
-        for (int i = 0; i < V; ++i) out.v[i] = from_f<T>(0.f);
+      for (int i = 0; i < V * TAPS / 4; ++i) {
+        const float4 q = __ldg(reinterpret_cast<const float4*>(pw) + i);
+        w[4 * i] = q.x, w[4 * i + 1] = q.y, w[4 * i + 2] = q.z, w[4 * i + 3] = q.w;
       }
-      *reinterpret_cast<Vt*>(y + (t + r) * p.yr) = out;
+    } else {
+#pragma unroll
+      for (int j = 0; j < TAPS; ++j) w[j] = __ldg(pw + j);
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i) bias[i] = p.bias ? __ldg(p.bias + c + i) : 0.f;
+    for (int t = t0; t < tv; t += R) {
+      Row next[R];
+      if (t + R < tv) {
+#pragma unroll
+        for (int r = 0; r < R; ++r) next[r].load(x + min(t + R + r, tv - 1) * p.xr);
+      }
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        if (t + r < tv) {
+          float out[V];
+#pragma unroll
+          for (int i = 0; i < V; ++i) {
+            float acc = bias[i];
+            // taps 0 .. H - 1 meet rows t + r - H .. t + r - 1: the history, then this batch's rows
+#pragma unroll
+            for (int j = 0; j < H; ++j) acc = fmaf(w[i * TAPS + j], r + j < H ? h[r + j < H ? r + j : 0].get(i) : in[r + j >= H ? r + j - H : 0].get(i), acc);
+            acc = fmaf(w[i * TAPS + H], in[r].get(i), acc);
+            out[i] = p.act == GAM_ACT_SWISH ? swish_f(acc) : acc;
+          }
+          Row o;
+          o.set(out);
+          o.store(y + (t + r) * p.yr);
+        }
+      }
+      // the last H rows seen
+#pragma unroll
+      for (int j = 0; j < H; ++j) {
+        if (R + j < H) h[j] = h[R + j < H ? R + j : 0];
+        else h[j] = in[R + j - H < R && R + j >= H ? R + j - H : 0];
+      }
+#pragma unroll
+      for (int r = 0; r < R; ++r) in[r] = next[r];
     }
   }
+  Row zero;
+  zero.zero();
+  for (int t = max(t0, len); t < t1; ++t) zero.store(y + t * p.yr);
 }
 
-template <typename T, int V>
-cudaError_t launch_taps(int taps, dim3 grid, const ConvArgs& p, cudaStream_t s) {
+template <typename T, int V, int R>
+cudaError_t launch_taps(int taps, unsigned grid, const ConvArgs& p, cudaStream_t s) {
   switch (taps) {
-    case 2: short_conv_kernel<T, V, 2><<<grid, kThreads, 0, s>>>(p); break;
-    case 3: short_conv_kernel<T, V, 3><<<grid, kThreads, 0, s>>>(p); break;
-    case 4: short_conv_kernel<T, V, 4><<<grid, kThreads, 0, s>>>(p); break;
-    case 5: short_conv_kernel<T, V, 5><<<grid, kThreads, 0, s>>>(p); break;
-    case 6: short_conv_kernel<T, V, 6><<<grid, kThreads, 0, s>>>(p); break;
-    case 7: short_conv_kernel<T, V, 7><<<grid, kThreads, 0, s>>>(p); break;
-    default: short_conv_kernel<T, V, 8><<<grid, kThreads, 0, s>>>(p); break;
+    case 2: short_conv_kernel<T, V, 2, R><<<grid, kThreads, 0, s>>>(p); break;
+    case 3: short_conv_kernel<T, V, 3, R><<<grid, kThreads, 0, s>>>(p); break;
+    case 4: short_conv_kernel<T, V, 4, R><<<grid, kThreads, 0, s>>>(p); break;
+    case 5: short_conv_kernel<T, V, 5, R><<<grid, kThreads, 0, s>>>(p); break;
+    case 6: short_conv_kernel<T, V, 6, R><<<grid, kThreads, 0, s>>>(p); break;
+    case 7: short_conv_kernel<T, V, 7, R><<<grid, kThreads, 0, s>>>(p); break;
+    default: short_conv_kernel<T, V, 8, R><<<grid, kThreads, 0, s>>>(p); break;
   }
   return cudaGetLastError();
 }
 
 template <typename T>
-gam_status launch(int taps, int batch, ConvArgs p, int sms, cudaStream_t s) {
-  constexpr int VW = 16 / sizeof(T);
+gam_status launch(int taps, ConvArgs p, int sms, cudaStream_t s) {
+  constexpr int VW = 16 / sizeof(T), R = 8;
   const bool wide = p.d % VW == 0 && aligned(p.x, 16) && aligned(p.y, 16) && aligned(p.state_in, 16) &&
-                    aligned(p.state_out, 16) && p.xb % VW == 0 && p.xr % VW == 0 && p.yb % VW == 0 && p.yr % VW == 0;
-  const int V = wide ? VW : 1;
-  p.cblocks = (p.d / V + kThreads - 1) / kThreads;
-  // segments: enough CTAs for 8 to an SM, none shorter than 16 rows
-  const int64_t base = (int64_t)p.cblocks * batch, want = (int64_t)sms * 8;
-  int64_t segs = (want + base - 1) / base;
-  const int64_t most = p.t_max / 16 > 1 ? p.t_max / 16 : 1;
-  if (segs > most) segs = most;
-  p.seg = p.t_max ? (int)((p.t_max + segs - 1) / segs) : 1;
-  p.seg = (p.seg + 7) / 8 * 8;
+                    aligned(p.state_out, 16) && aligned(p.w, 16) && p.xb % VW == 0 && p.xr % VW == 0 &&
+                    p.yb % VW == 0 && p.yr % VW == 0;
+  p.vecs = wide ? p.d / VW : p.d;
+  // segments of R .. rows: short enough for 512 threads to an SM
+  const int64_t columns = (int64_t)p.vecs * p.batch, want = (int64_t)sms * 512;
+  const int64_t segs = std::max<int64_t>(1, std::min<int64_t>((want + columns - 1) / columns, p.t_max / R));
+  p.seg = std::max(R, (int)((p.t_max + segs - 1) / segs + R - 1) / R * R);
   p.segs = p.t_max ? (p.t_max + p.seg - 1) / p.seg : 1;
-  const int64_t grid = base * p.segs;
+  const int64_t grid = (columns * p.segs + kThreads - 1) / kThreads;
   if (grid > INT32_MAX) return op_fail(GAM_ERR_CAPACITY, "batch * t_max * d too large for one call");
-  return launch_status(wide ? launch_taps<T, VW>(taps, dim3((unsigned)grid), p, s)
-                            : launch_taps<T, 1>(taps, dim3((unsigned)grid), p, s));
+  const unsigned g = (unsigned)grid;
+  if (p.t_max == 1)
+    return launch_status(wide ? launch_taps<T, VW, 1>(taps, g, p, s) : launch_taps<T, 1, 1>(taps, g, p, s));
+  return launch_status(wide ? launch_taps<T, VW, R>(taps, g, p, s) : launch_taps<T, 1, R>(taps, g, p, s));
 }
 
 }  // namespace
@@ -167,10 +182,10 @@ extern "C" gam_status gam_short_conv(const void* x, int dtype, int64_t x_batch_s
     int sms = 0;
     if (gam_status st = check_device(&sms)) return st;
     ConvArgs p{x,  w, bias, lengths, state_in, state_out, y, x_batch_stride, x_row_stride, y_batch_stride, y_row_stride,
-               act, t_max, d, 0, 0, 0};
+               act, batch, t_max, d, 0, 0, 0};
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if (dtype == GAM_DTYPE_F32) return launch<float>(taps, batch, p, sms, s);
-    if (dtype == GAM_DTYPE_F16) return launch<__half>(taps, batch, p, sms, s);
-    return launch<bf16>(taps, batch, p, sms, s);
+    if (dtype == GAM_DTYPE_F32) return launch<float>(taps, p, sms, s);
+    if (dtype == GAM_DTYPE_F16) return launch<__half>(taps, p, sms, s);
+    return launch<bf16>(taps, p, sms, s);
   });
 }

@@ -7,6 +7,7 @@
 #include <cuda_fp16.h>
 
 #include <string>
+#include <type_traits>
 
 #include "../../include/gam.h"
 #include "common.cuh"
@@ -32,6 +33,72 @@ __device__ __forceinline__ bf16 from_f<bf16>(float v) { return __float2bfloat16_
 template <typename T, int V>
 struct alignas(sizeof(T) * V < 16 ? sizeof(T) * V : 16) Vec {
   T v[V];
+};
+
+// V values as they lie in memory.  A load waits for nothing and converts nothing, so
+// that a thread can have many of them on their way; get(k) converts value k.
+template <typename T, int V>
+struct Raw {
+  static constexpr int BYTES = V * sizeof(T), N = BYTES >= 4 ? BYTES / 4 : 1;
+  static_assert(BYTES <= 4 || BYTES % 16 == 0, "one value, a pair of 16 bits, or whole 16-byte accesses");
+  uint32_t w[N];
+  __device__ __forceinline__ void load(const T* p) {
+    if constexpr (BYTES < 4) {
+      w[0] = *reinterpret_cast<const unsigned short*>(p);
+    } else if constexpr (BYTES == 4) {
+      w[0] = *reinterpret_cast<const uint32_t*>(p);
+    } else {
+#pragma unroll
+      for (int i = 0; i < N / 4; ++i) {
+        const uint4 q = reinterpret_cast<const uint4*>(p)[i];
+        w[4 * i] = q.x, w[4 * i + 1] = q.y, w[4 * i + 2] = q.z, w[4 * i + 3] = q.w;
+      }
+    }
+  }
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int i = 0; i < N; ++i) w[i] = 0;
+  }
+  __device__ __forceinline__ void store(T* p) const {
+    if constexpr (BYTES < 4) {
+      *reinterpret_cast<unsigned short*>(p) = (unsigned short)w[0];
+    } else if constexpr (BYTES == 4) {
+      *reinterpret_cast<uint32_t*>(p) = w[0];
+    } else {
+#pragma unroll
+      for (int i = 0; i < N / 4; ++i)
+        reinterpret_cast<uint4*>(p)[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+    }
+  }
+  __device__ __forceinline__ float get(int k) const {
+    if constexpr (sizeof(T) == 4) {
+      return __uint_as_float(w[k]);
+    } else {
+      const uint32_t u = w[k / 2];
+      if constexpr (std::is_same_v<T, bf16>) return __uint_as_float((k & 1) ? u & 0xffff0000u : u << 16);
+      else return __half2float(__ushort_as_half((unsigned short)((k & 1) ? u >> 16 : u)));
+    }
+  }
+  __device__ __forceinline__ void set(const float (&v)[V]) {
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) w[i] = __float_as_uint(v[i]);
+    } else if constexpr (V == 1) {
+      const T t = from_f<T>(v[0]);
+      w[0] = *reinterpret_cast<const unsigned short*>(&t);
+    } else {
+#pragma unroll
+      for (int i = 0; i < V / 2; ++i) {
+        if constexpr (std::is_same_v<T, bf16>) {
+          const __nv_bfloat162 q = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+          w[i] = *reinterpret_cast<const uint32_t*>(&q);
+        } else {
+          const __half2 q = __floats2half2_rn(v[2 * i], v[2 * i + 1]);
+          w[i] = *reinterpret_cast<const uint32_t*>(&q);
+        }
+      }
+    }
+  }
 };
 
 __device__ __forceinline__ float sigmoid_f(float v) { return 1.f / (1.f + __expf(-v)); }
