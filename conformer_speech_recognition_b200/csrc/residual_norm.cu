@@ -160,12 +160,16 @@ gam_status launch_v(const gam_residual_norm_args& p, int64_t per_gate, int sms, 
   if (p.rows > INT32_MAX) return op_fail(GAM_ERR_CAPACITY, "too many rows for one call");
   const unsigned grid = (unsigned)p.rows;
   auto threads = [&](int nv) { return ((vecs + nv - 1) / nv + 31) / 32 * 32; };
+  // as few accesses to a thread as the CTA's size allows
   if (vecs <= 512) residual_norm_kernel<TX, TY, false, V, 1><<<grid, threads(1), 0, s>>>(p, per_gate);
   else if (vecs <= 1024) residual_norm_kernel<TX, TY, false, V, 2><<<grid, threads(2), 0, s>>>(p, per_gate);
   else if (vecs <= 2048) residual_norm_kernel<TX, TY, false, V, 4><<<grid, threads(4), 0, s>>>(p, per_gate);
   else if constexpr (V < 8) {
-    if (vecs <= 4096) residual_norm_kernel<TX, TY, false, V, V == 1 ? 8 : 4><<<grid, threads(V == 1 ? 8 : 4), 0, s>>>(p, per_gate);
-    else if constexpr (V == 1) residual_norm_kernel<TX, TY, false, V, 16><<<grid, threads(16), 0, s>>>(p, per_gate);
+    if (vecs <= 4096) residual_norm_kernel<TX, TY, false, V, 4><<<grid, threads(4), 0, s>>>(p, per_gate);
+    else if constexpr (V == 1) {
+      if (vecs <= 8192) residual_norm_kernel<TX, TY, false, V, 8><<<grid, threads(8), 0, s>>>(p, per_gate);
+      else residual_norm_kernel<TX, TY, false, V, 16><<<grid, threads(16), 0, s>>>(p, per_gate);
+    }
   }
   return launch_status(cudaGetLastError());
 }

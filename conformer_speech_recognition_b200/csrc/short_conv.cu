@@ -137,22 +137,24 @@ cudaError_t launch_taps(int taps, unsigned grid, const ConvArgs& p, cudaStream_t
 
 template <typename T>
 gam_status launch(int taps, ConvArgs p, int sms, cudaStream_t s) {
-  constexpr int VW = 16 / sizeof(T), R = 8;
+  constexpr int VW = 16 / sizeof(T);
   const bool wide = p.d % VW == 0 && aligned(p.x, 16) && aligned(p.y, 16) && aligned(p.state_in, 16) &&
                     aligned(p.state_out, 16) && aligned(p.w, 16) && p.xb % VW == 0 && p.xr % VW == 0 &&
                     p.yb % VW == 0 && p.yr % VW == 0;
   p.vecs = wide ? p.d / VW : p.d;
-  // segments of R .. rows: short enough for 512 threads to an SM
+  // Segments short enough for 512 threads to an SM, of 8 rows on their way at a time; a call too small for
+  // that takes 2 rows to a thread, since one warp's instructions then are its time.
   const int64_t columns = (int64_t)p.vecs * p.batch, want = (int64_t)sms * 512;
-  const int64_t segs = std::max<int64_t>(1, std::min<int64_t>((want + columns - 1) / columns, p.t_max / R));
+  const int64_t segs = std::max<int64_t>(1, (want + columns - 1) / columns);
+  const int R = p.t_max == 1 ? 1 : p.t_max / segs >= 8 ? 8 : 2;
   p.seg = std::max(R, (int)((p.t_max + segs - 1) / segs + R - 1) / R * R);
   p.segs = p.t_max ? (p.t_max + p.seg - 1) / p.seg : 1;
   const int64_t grid = (columns * p.segs + kThreads - 1) / kThreads;
   if (grid > INT32_MAX) return op_fail(GAM_ERR_CAPACITY, "batch * t_max * d too large for one call");
   const unsigned g = (unsigned)grid;
-  if (p.t_max == 1)
-    return launch_status(wide ? launch_taps<T, VW, 1>(taps, g, p, s) : launch_taps<T, 1, 1>(taps, g, p, s));
-  return launch_status(wide ? launch_taps<T, VW, R>(taps, g, p, s) : launch_taps<T, 1, R>(taps, g, p, s));
+  if (R == 1) return launch_status(wide ? launch_taps<T, VW, 1>(taps, g, p, s) : launch_taps<T, 1, 1>(taps, g, p, s));
+  if (R == 2) return launch_status(wide ? launch_taps<T, VW, 2>(taps, g, p, s) : launch_taps<T, 1, 2>(taps, g, p, s));
+  return launch_status(wide ? launch_taps<T, VW, 8>(taps, g, p, s) : launch_taps<T, 1, 8>(taps, g, p, s));
 }
 
 }  // namespace

@@ -101,8 +101,14 @@ struct Raw {
   }
 };
 
-__device__ __forceinline__ float sigmoid_f(float v) { return 1.f / (1.f + __expf(-v)); }
-__device__ __forceinline__ float swish_f(float v) { return v / (1.f + __expf(-v)); }
+// The hardware's reciprocal (1 step off) in place of a division, which takes several
+// times the instructions; e^-v overflowing to infinity gives 0, the right limit.
+__device__ __forceinline__ float sigmoid_f(float v) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + __expf(-v)));
+  return r;
+}
+__device__ __forceinline__ float swish_f(float v) { return v * sigmoid_f(v); }
 
 __device__ __forceinline__ float activate(float v, int act) {
   switch (act) {
