@@ -68,20 +68,29 @@ __global__ void __launch_bounds__(kThreads) short_conv_kernel(const ConvArgs p) 
     for (int j = 0; j < H; ++j) keep[j].store(so + (int64_t)j * p.d);
   }
   if (work) {
-    float w[V * TAPS], bias[V];                // w[i TAPS + j]: channel i, tap j
+    constexpr int P = V > 1 ? V / 2 : 1;       // pairs of channels (a single one in both halves)
+    constexpr int B = V > 1 ? 1 : 0;
+    float wf[V * TAPS];                        // channel i, tap j at i TAPS + j
     const float* pw = p.w + (int64_t)c * TAPS;
     if constexpr (V > 1) {                     // 16-byte aligned with the rows
 #pragma unroll
       for (int i = 0; i < V * TAPS / 4; ++i) {
         const float4 q = __ldg(reinterpret_cast<const float4*>(pw) + i);
-        w[4 * i] = q.x, w[4 * i + 1] = q.y, w[4 * i + 2] = q.z, w[4 * i + 3] = q.w;
+        wf[4 * i] = q.x, wf[4 * i + 1] = q.y, wf[4 * i + 2] = q.z, wf[4 * i + 3] = q.w;
       }
     } else {
 #pragma unroll
-      for (int j = 0; j < TAPS; ++j) w[j] = __ldg(pw + j);
+      for (int j = 0; j < TAPS; ++j) wf[j] = __ldg(pw + j);
     }
+    u64 w[TAPS][P], bias[P], v[H][P];          // v: the last H rows, oldest first
 #pragma unroll
-    for (int i = 0; i < V; ++i) bias[i] = p.bias ? __ldg(p.bias + c + i) : 0.f;
+    for (int i = 0; i < P; ++i) {
+#pragma unroll
+      for (int j = 0; j < TAPS; ++j) w[j][i] = pack2(wf[2 * i * TAPS + j], wf[(2 * i + B) * TAPS + j]);
+      bias[i] = p.bias ? pack2(__ldg(p.bias + c + 2 * i), __ldg(p.bias + c + 2 * i + B)) : 0ull;
+#pragma unroll
+      for (int j = 0; j < H; ++j) v[j][i] = pack2(h[j].get(2 * i), h[j].get(2 * i + B));
+    }
     for (int t = t0; t < tv; t += R) {
       Row next[R];
       if (t + R < tv) {
@@ -90,27 +99,26 @@ __global__ void __launch_bounds__(kThreads) short_conv_kernel(const ConvArgs p) 
       }
 #pragma unroll
       for (int r = 0; r < R; ++r) {
+        float out[V];
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+          const u64 cur = pack2(in[r].get(2 * i), in[r].get(2 * i + B));
+          u64 acc = bias[i];
+#pragma unroll
+          for (int j = 0; j < H; ++j) acc = fma2(w[j][i], v[j][i], acc);
+          acc = fma2(w[H][i], cur, acc);
+#pragma unroll
+          for (int j = 0; j + 1 < H; ++j) v[j][i] = v[j + 1][i];
+          v[H - 1][i] = cur;
+          const float2 q = unpack2(acc);
+          out[2 * i] = p.act == GAM_ACT_SWISH ? swish_f(q.x) : q.x;
+          if constexpr (V > 1) out[2 * i + 1] = p.act == GAM_ACT_SWISH ? swish_f(q.y) : q.y;
+        }
         if (t + r < tv) {
-          float out[V];
-#pragma unroll
-          for (int i = 0; i < V; ++i) {
-            float acc = bias[i];
-            // taps 0 .. H - 1 meet rows t + r - H .. t + r - 1: the history, then this batch's rows
-#pragma unroll
-            for (int j = 0; j < H; ++j) acc = fmaf(w[i * TAPS + j], r + j < H ? h[r + j < H ? r + j : 0].get(i) : in[r + j >= H ? r + j - H : 0].get(i), acc);
-            acc = fmaf(w[i * TAPS + H], in[r].get(i), acc);
-            out[i] = p.act == GAM_ACT_SWISH ? swish_f(acc) : acc;
-          }
           Row o;
           o.set(out);
           o.store(y + (t + r) * p.yr);
         }
-      }
-      // the last H rows seen
-#pragma unroll
-      for (int j = 0; j < H; ++j) {
-        if (R + j < H) h[j] = h[R + j < H ? R + j : 0];
-        else h[j] = in[R + j - H < R && R + j >= H ? R + j - H : 0];
       }
 #pragma unroll
       for (int r = 0; r < R; ++r) in[r] = next[r];

@@ -35,18 +35,46 @@ struct alignas(sizeof(T) * V < 16 ? sizeof(T) * V : 16) Vec {
   T v[V];
 };
 
+// Packed fp32 (sm_100 f32x2): a 64-bit register holds two values, one instruction does both.
+using u64 = unsigned long long;
+
+__device__ __forceinline__ u64 pack2(float a, float b) {
+  u64 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float2 unpack2(u64 v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ u64 fma2(u64 a, u64 b, u64 c) {
+  u64 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ u64 mul2(u64 a, u64 b) {
+  u64 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ u64 both(float v) { return pack2(v, v); }
+
 // V values as they lie in memory.  A load waits for nothing and converts nothing, so
 // that a thread can have many of them on their way; get(k) converts value k.
 template <typename T, int V>
 struct Raw {
   static constexpr int BYTES = V * sizeof(T), N = BYTES >= 4 ? BYTES / 4 : 1;
-  static_assert(BYTES <= 4 || BYTES % 16 == 0, "one value, a pair of 16 bits, or whole 16-byte accesses");
+  static_assert(BYTES <= 8 || BYTES % 16 == 0, "one value, a pair, or whole 16-byte accesses");
   uint32_t w[N];
   __device__ __forceinline__ void load(const T* p) {
     if constexpr (BYTES < 4) {
       w[0] = *reinterpret_cast<const unsigned short*>(p);
     } else if constexpr (BYTES == 4) {
       w[0] = *reinterpret_cast<const uint32_t*>(p);
+    } else if constexpr (BYTES == 8) {
+      const uint2 q = *reinterpret_cast<const uint2*>(p);
+      w[0] = q.x, w[1] = q.y;
     } else {
 #pragma unroll
       for (int i = 0; i < N / 4; ++i) {
@@ -64,6 +92,8 @@ struct Raw {
       *reinterpret_cast<unsigned short*>(p) = (unsigned short)w[0];
     } else if constexpr (BYTES == 4) {
       *reinterpret_cast<uint32_t*>(p) = w[0];
+    } else if constexpr (BYTES == 8) {
+      *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
     } else {
 #pragma unroll
       for (int i = 0; i < N / 4; ++i)
