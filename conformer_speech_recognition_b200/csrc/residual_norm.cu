@@ -24,152 +24,158 @@ namespace {
 // Sum over the G threads of a row: a warp by shuffles, a CTA through shared
 // memory (red holds two alternating sets of 32 partial sums, so one barrier per
 // sum is enough).
-template <bool WARP>
+template <int G>
 __device__ __forceinline__ float row_sum(float v, float (*red)[32], int& turn) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  if constexpr (WARP) return v;
-  const int lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+  if constexpr (G == 32) return v;
+  const int lane = threadIdx.x & 31;
   float* r = red[turn];
   turn ^= 1;
   if (lane == 0) r[threadIdx.x >> 5] = v;
   __syncthreads();
-  v = lane < warps ? r[lane] : 0.f;
+  v = lane < G / 32 ? r[lane] : 0.f;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  return v;
+  for (int o = G / 64; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return __shfl_sync(0xffffffffu, v, 0);
 }
 
-// Row position of a thread: it holds accesses j G + tid of V columns, j < NV, the first
-// column of an access being `phase` (pairs only) before its multiple of V.
-template <int V>
+// A thread's part of a row: accesses j < NV of V columns from j G V + first on, first being
+// its own multiple of V less the phase (pairs).  G is known at compile time, so that an
+// access is one base register and a constant.  Only a pair can lie partly beside the row.
+template <int G, int V>
 struct Place {
-  int tid, G, d, phase;
-  __device__ __forceinline__ int col(int j) const { return (j * G + tid) * V - (V == 2 ? phase : 0); }
-  __device__ __forceinline__ bool on(int j, int i) const {  // value i of access j is a column of the row
-    const int c = col(j) + i;
-    return V == 2 ? (unsigned)c < (unsigned)d : c < d;
-  }
-  __device__ __forceinline__ bool whole(int j) const { return V == 2 ? on(j, 0) && on(j, 1) : on(j, 0); }
+  int first, d;
+  __device__ __forceinline__ bool on(int j, int i) const { return (unsigned)(first + j * G * V + i) < (unsigned)d; }
+  __device__ __forceinline__ bool whole(int j) const { return on(j, 0) && (V != 2 || on(j, 1)); }
 };
 
-// Access j of a row; what lies beside the row is 0 and not read.
-template <typename T, int V>
-__device__ __forceinline__ void load_at(Raw<T, V>& r, const T* row, const Place<V>& at, int j) {
-  r.zero();
-  if (at.whole(j)) r.load(row + at.col(j));
-}
-// ... the halves of a pair at the row's ends (after all whole accesses are on their way)
-template <typename T, int V>
-__device__ __forceinline__ void load_ends(Raw<T, V>& r, const T* row, const Place<V>& at, int j) {
+// The row's values; 0 for what lies beside it, which is not read.  Whole accesses first,
+// then the halves of cut pairs, so that nothing waits on the way.
+template <int G, int V, int NV, typename T>
+__device__ __forceinline__ void load_row(Raw<T, V> (&r)[NV], const T* row, const Place<G, V>& at) {
+  const T* mine = row + at.first;
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    r[j].zero();
+    if (at.whole(j)) r[j].load(mine + j * G * V);
+  }
   if constexpr (V == 2) {
-    if (!at.whole(j) && (at.on(j, 0) || at.on(j, 1))) {
-      const int i = at.on(j, 1);
-      Raw<T, 1> one;
-      one.load(row + at.col(j) + i);
-      if constexpr (sizeof(T) == 4) r.w[i] = one.w[0];
-      else r.w[0] = one.w[0] << (16 * i);
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+      if (at.on(j, 0) != at.on(j, 1)) {
+        const int i = at.on(j, 1);
+        Raw<T, 1> one;
+        one.load(mine + j * G * V + i);
+        if constexpr (sizeof(T) == 4) r[j].w[i] = one.w[0];
+        else r[j].w[0] = one.w[0] << (16 * i);
+      }
+  }
+}
+template <int G, int V, int NV, typename T>
+__device__ __forceinline__ void store_row(T* row, const Place<G, V>& at, const float (&v)[NV][V]) {
+  T* mine = row + at.first;
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    if (at.whole(j)) {
+      Raw<T, V> o;
+      o.set(v[j]);
+      o.store(mine + j * G * V);
+    } else if constexpr (V == 2) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        if (at.on(j, i)) mine[j * G * V + i] = from_f<T>(v[j][i]);
     }
   }
 }
-template <typename T, int V>
-__device__ __forceinline__ void store_at(T* row, const Place<V>& at, int j, const float (&v)[V]) {
-  if (at.whole(j)) {
-    Raw<T, V> o;
-    o.set(v);
-    o.store(row + at.col(j));
-  } else if constexpr (V == 2) {
+// Access j of a parameter vector [d]; 0 beside the row.
+template <int G, int V>
+__device__ __forceinline__ void load_param(float (&out)[V], const float* p, const Place<G, V>& at, int j) {
+  const float* mine = p + at.first + j * G * V;
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
-      if (at.on(j, i)) row[at.col(j) + i] = from_f<T>(v[i]);
-  }
-}
-
-template <int V>
-__device__ __forceinline__ void load_param(const float* p, const Place<V>& at, int j, float fill, float (&out)[V]) {
-  const int c = at.col(j);
+  for (int i = 0; i < V; ++i) out[i] = 0.f;
   if constexpr (V <= 2) {
 #pragma unroll
-    for (int i = 0; i < V; ++i) out[i] = p ? __ldg(p + min(max(c + i, 0), at.d - 1)) : fill;
-  } else {  // 16-byte aligned with the rows
-    const float* q = p + min(c, at.d - V);
+    for (int i = 0; i < V; ++i)
+      if (at.on(j, i)) out[i] = __ldg(mine + i);
+  } else if (at.whole(j)) {  // 16-byte aligned with the rows
 #pragma unroll
     for (int i = 0; i < V / 4; ++i) {
-      const float4 f = p ? __ldg(reinterpret_cast<const float4*>(q) + i) : make_float4(fill, fill, fill, fill);
+      const float4 f = __ldg(reinterpret_cast<const float4*>(mine) + i);
       out[4 * i] = f.x, out[4 * i + 1] = f.y, out[4 * i + 2] = f.z, out[4 * i + 3] = f.w;
     }
   }
 }
 
-// v <- norm(v) over the row
-template <bool WARP, int V, int NV>
-__device__ __forceinline__ void norm_row(float (&v)[NV][V], int kind, const float* w, const float* b, float eps,
-                                         const Place<V>& at, float (*red)[32], int& turn) {
+// v <- norm(v) over the row; v is 0 beside it, before and after.
+template <int G, int V, int NV>
+__device__ __forceinline__ void norm_row(float (&v)[NV][V], bool layer, const float* w, const float* b, float eps,
+                                         const Place<G, V>& at, float (*red)[32], int& turn) {
   // one access a thread: its weights come while the row is summed
   float w0[V], b0[V];
   if constexpr (NV == 1) {
-    load_param<V>(w, at, 0, 1.f, w0);
-    load_param<V>(kind == GAM_NORM_LAYER ? b : nullptr, at, 0, 0.f, b0);
+    if (w) load_param<G, V>(w0, w, at, 0);
+    if (b) load_param<G, V>(b0, b, at, 0);
   }
   const float inv = 1.f / at.d;
-  if (kind == GAM_NORM_LAYER) {
+  if (layer) {
     float s = 0.f;
 #pragma unroll
     for (int j = 0; j < NV; ++j)
 #pragma unroll
       for (int i = 0; i < V; ++i) s += v[j][i];
-    const float mean = row_sum<WARP>(s, red, turn) * inv;
+    const float mean = row_sum<G>(s, red, turn) * inv;
 #pragma unroll
     for (int j = 0; j < NV; ++j)
 #pragma unroll
-      for (int i = 0; i < V; ++i) v[j][i] = at.on(j, i) ? v[j][i] - mean : 0.f;
+      for (int i = 0; i < V; ++i) v[j][i] = at.on(j, V == 2 ? i : 0) ? v[j][i] - mean : 0.f;
   }
   float q = 0.f;
 #pragma unroll
   for (int j = 0; j < NV; ++j)
 #pragma unroll
     for (int i = 0; i < V; ++i) q = fmaf(v[j][i], v[j][i], q);
-  const float r = rsqrtf(fmaf(row_sum<WARP>(q, red, turn), inv, eps));
+  const float r = rsqrtf(fmaf(row_sum<G>(q, red, turn), inv, eps));
 #pragma unroll
-  for (int j = 0; j < NV; ++j) {
-    if constexpr (NV > 1) {
-      load_param<V>(w, at, j, 1.f, w0);
-      load_param<V>(kind == GAM_NORM_LAYER ? b : nullptr, at, j, 0.f, b0);
+  for (int j = 0; j < NV; ++j)
+#pragma unroll
+    for (int i = 0; i < V; ++i) v[j][i] *= r;
+  if (w)
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      if constexpr (NV > 1) load_param<G, V>(w0, w, at, j);
+#pragma unroll
+      for (int i = 0; i < V; ++i) v[j][i] *= w0[i];
     }
+  if (b)
 #pragma unroll
-    for (int i = 0; i < V; ++i) v[j][i] = at.on(j, i) ? fmaf(v[j][i] * r, w0[i], b0[i]) : 0.f;
-  }
+    for (int j = 0; j < NV; ++j) {
+      if constexpr (NV > 1) load_param<G, V>(b0, b, at, j);
+#pragma unroll
+      for (int i = 0; i < V; ++i) v[j][i] += b0[i];
+    }
 }
 
 constexpr int kWarps = 4;  // rows of a CTA at a time in the warp form
 
-template <typename TX, typename TY, bool WARP, int V, int NV, bool GATE>
-__global__ void __launch_bounds__(WARP ? 32 * kWarps : V == 8 ? 512 : 1024, WARP && NV == 4 ? 3 : 1)
+template <typename TX, typename TY, int G, int V, int NV, bool GATE>
+__global__ void __launch_bounds__(G == 32 ? 32 * kWarps : G, G == 32 ? (NV == 4 ? 3 : 5) : NV * V <= 12 ? 1024 / G : 1)
 residual_norm_kernel(const gam_residual_norm_args p, const int64_t per_gate) {
+  constexpr bool WARP = G == 32;
   __shared__ float red[2][32];
   const int64_t step = WARP ? (int64_t)gridDim.x * kWarps : (int64_t)gridDim.x;
   int64_t row = WARP ? (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5) : (int64_t)blockIdx.x;
-  Place<V> at{(int)(WARP ? threadIdx.x & 31 : threadIdx.x), (int)(WARP ? 32 : blockDim.x), p.d, 0};
+  const int own = (int)(WARP ? threadIdx.x & 31 : threadIdx.x) * V;
+  const float* post_b = p.post_norm == GAM_NORM_LAYER ? p.post_bias : nullptr;
+  const float* pre_b = p.pre_norm == GAM_NORM_LAYER ? p.pre_bias : nullptr;
+  Place<G, V> at{own, p.d};
   Raw<TX, V> rx[NV];
   Raw<TY, V> ry[NV], rg[GATE ? NV : 1];
   auto fetch = [&](int64_t r) {
-    const TX* xr = (const TX*)p.x + r * p.x_stride;
-    const TY* yr = (const TY*)p.y + r * p.y_stride;
-    const TY* gr = GATE ? (const TY*)p.gate + r / per_gate * p.gate_stride : nullptr;
-    at.phase = (int)(r * p.y_stride) & 1;
-#pragma unroll
-    for (int j = 0; j < NV; ++j) load_at<TY, V>(ry[j], yr, at, j);
-#pragma unroll
-    for (int j = 0; j < NV; ++j) load_at<TX, V>(rx[j], xr, at, j);
-    if constexpr (GATE)
-#pragma unroll
-      for (int j = 0; j < NV; ++j) load_at<TY, V>(rg[j], gr, at, j);
-#pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      load_ends<TY, V>(ry[j], yr, at, j);
-      load_ends<TX, V>(rx[j], xr, at, j);
-      if constexpr (GATE) load_ends<TY, V>(rg[j], gr, at, j);
-    }
+    if constexpr (V == 2) at.first = own - ((int)(r * p.y_stride) & 1);
+    load_row<G, V, NV>(ry, (const TY*)p.y + r * p.y_stride, at);
+    load_row<G, V, NV>(rx, (const TX*)p.x + r * p.x_stride, at);
+    if constexpr (GATE) load_row<G, V, NV>(rg, (const TY*)p.gate + r / per_gate * p.gate_stride, at);
   };
   if (row >= p.rows) return;
   fetch(row);
@@ -184,24 +190,41 @@ residual_norm_kernel(const gam_residual_norm_args p, const int64_t per_gate) {
         x[j][i] = rx[j].get(i);
         if constexpr (GATE) g[j][i] = rg[j].get(i);
       }
-    const Place<V> here = at;
+    const Place<G, V> here = at;
     if (WARP && row + step < p.rows) fetch(row + step);
-    if (p.post_norm) norm_row<WARP, V, NV>(y, p.post_norm, p.post_weight, p.post_bias, p.eps, here, red, turn);
+    if (p.post_norm)
+      norm_row<G, V, NV>(y, p.post_norm == GAM_NORM_LAYER, p.post_weight, post_b, p.eps, here, red, turn);
+    if constexpr (GATE) {
+      auto gate = [&](auto act) {
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      float ls[V];
-      load_param<V>(p.layer_scale, here, j, 1.f, ls);
+        for (int j = 0; j < NV; ++j)
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
-        if constexpr (GATE) y[j][i] *= activate(g[j][i], p.gate_act);
-        x[j][i] = here.on(j, i) ? fmaf(p.alpha * ls[i], y[j][i], x[j][i]) : 0.f;
+          for (int i = 0; i < V; ++i) y[j][i] *= act(g[j][i]);
+      };
+      switch (p.gate_act) {
+        case GAM_ACT_SWISH: gate([](float v) { return swish_f(v); }); break;
+        case GAM_ACT_SIGMOID: gate([](float v) { return sigmoid_f(v); }); break;
+        case GAM_ACT_TANH: gate([](float v) { return tanhf(v); }); break;
+        default: gate([](float v) { return v; });
       }
-      if (p.x_out) store_at<TX, V>((TX*)p.x_out + row * p.x_out_stride, here, j, x[j]);
     }
-    if (p.u) {
-      if (p.pre_norm) norm_row<WARP, V, NV>(x, p.pre_norm, p.pre_weight, p.pre_bias, p.eps, here, red, turn);
+    if (p.layer_scale)
 #pragma unroll
-      for (int j = 0; j < NV; ++j) store_at<TY, V>((TY*)p.u + row * p.u_stride, here, j, x[j]);
+      for (int j = 0; j < NV; ++j) {
+        float ls[V];
+        load_param<G, V>(ls, p.layer_scale, here, j);
+#pragma unroll
+        for (int i = 0; i < V; ++i) y[j][i] *= ls[i];
+      }
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+#pragma unroll
+      for (int i = 0; i < V; ++i) x[j][i] = fmaf(p.alpha, y[j][i], x[j][i]);
+    if (p.x_out) store_row<G, V, NV>((TX*)p.x_out + row * p.x_out_stride, here, x);
+    if (p.u) {
+      if (p.pre_norm)
+        norm_row<G, V, NV>(x, p.pre_norm == GAM_NORM_LAYER, p.pre_weight, pre_b, p.eps, here, red, turn);
+      store_row<G, V, NV>((TY*)p.u + row * p.u_stride, here, x);
     }
     row += step;
     if (!WARP || row >= p.rows) return;
@@ -210,30 +233,49 @@ residual_norm_kernel(const gam_residual_norm_args p, const int64_t per_gate) {
 
 template <typename TX, typename TY, int V, bool GATE>
 gam_status launch_v(const gam_residual_norm_args& p, int64_t per_gate, int sms, cudaStream_t s) {
-  const int vecs = (p.d + V - 1) / V + (V == 2);  // a phase can cut one pair in two
-  // rows enough for 8 warps to an SM: a warp holds a row, up to 4 accesses to a lane, and walks over the rows
-  if (vecs <= 128 && (p.rows >= 8 * sms || vecs <= 32)) {
-    auto grid = [&](int per_sm) { return (unsigned)std::min<int64_t>((p.rows + kWarps - 1) / kWarps, (int64_t)sms * per_sm); };
-    if (vecs <= 32) residual_norm_kernel<TX, TY, true, V, 1, GATE><<<grid(8), 32 * kWarps, 0, s>>>(p, per_gate);
-    else if (vecs <= 64) residual_norm_kernel<TX, TY, true, V, 2, GATE><<<grid(5), 32 * kWarps, 0, s>>>(p, per_gate);
-    else residual_norm_kernel<TX, TY, true, V, 4, GATE><<<grid(3), 32 * kWarps, 0, s>>>(p, per_gate);
-    return launch_status(cudaGetLastError());
-  }
   if (p.rows > INT32_MAX) return op_fail(GAM_ERR_CAPACITY, "too many rows for one call");
-  const unsigned grid = (unsigned)p.rows;
-  auto threads = [&](int nv) { return ((vecs + nv - 1) / nv + 31) / 32 * 32; };
-  // as few accesses to a thread as the CTA's size allows
-  if (vecs <= 512) residual_norm_kernel<TX, TY, false, V, 1, GATE><<<grid, threads(1), 0, s>>>(p, per_gate);
-  else if (vecs <= 1024) residual_norm_kernel<TX, TY, false, V, 2, GATE><<<grid, threads(2), 0, s>>>(p, per_gate);
-  else if (vecs <= 2048) residual_norm_kernel<TX, TY, false, V, 4, GATE><<<grid, threads(4), 0, s>>>(p, per_gate);
-  else if constexpr (V < 8) {
-    if (vecs <= 4096) residual_norm_kernel<TX, TY, false, V, 4, GATE><<<grid, threads(4), 0, s>>>(p, per_gate);
-    else if constexpr (V <= 2) {
-      if (vecs <= 8192) residual_norm_kernel<TX, TY, false, V, 8, GATE><<<grid, threads(8), 0, s>>>(p, per_gate);
-      else residual_norm_kernel<TX, TY, false, V, 16, GATE><<<grid, threads(16), 0, s>>>(p, per_gate);
+  const int vecs = (p.d + V - 1) / V + (V == 2);  // a phase can cut one pair in two
+  auto warps = [&](auto kernel, int per_sm) {     // warps walk over the rows
+    const int64_t groups = (p.rows + kWarps - 1) / kWarps;
+    kernel<<<(unsigned)std::min<int64_t>(groups, (int64_t)sms * per_sm), 32 * kWarps, 0, s>>>(p, per_gate);
+    return launch_status(cudaGetLastError());
+  };
+  auto cta = [&](auto kernel, int threads) {      // a CTA to a row; walking over them was slower
+    kernel<<<(unsigned)p.rows, threads, 0, s>>>(p, per_gate);
+    return launch_status(cudaGetLastError());
+  };
+#define GAM_WARPS(NV, PER_SM) return warps(residual_norm_kernel<TX, TY, 32, V, NV, GATE>, PER_SM)
+#define GAM_CTA(G, NV) return cta(residual_norm_kernel<TX, TY, G, V, NV, GATE>, G)
+  // Rows enough for 8 warps to an SM: a warp holds a row, up to 4 accesses to a lane; else a CTA holds it.
+  const bool many = p.rows >= 8 * sms;
+  if constexpr (V > 2) {
+    if (vecs <= 32) GAM_WARPS(1, 8);
+    if (vecs <= 64 && many) GAM_WARPS(2, 5);
+    if (vecs <= 128 && many) GAM_WARPS(4, 3);
+    if (vecs <= 128) GAM_CTA(128, 1);
+    if (vecs <= 256) GAM_CTA(256, 1);
+    if (vecs <= 512) GAM_CTA(512, 1);
+    if (vecs <= 768) GAM_CTA(256, 3);
+    if (vecs <= 1024) GAM_CTA(512, 2);
+    if constexpr (V == 4) {
+      if (vecs > 2048) GAM_CTA(512, 8);
     }
+    GAM_CTA(512, 4);
+  } else if constexpr (V == 2) {
+    if (vecs <= 32) GAM_WARPS(1, 8);
+    if (vecs <= 128 && many) GAM_WARPS(4, 3);
+    if (vecs <= 384) GAM_CTA(128, 3);
+    if (vecs <= 768) GAM_CTA(256, 3);
+    if (vecs <= 1536) GAM_CTA(512, 3);
+    if (vecs <= 2560) GAM_CTA(512, 5);
+    if (vecs <= 4096) GAM_CTA(512, 8);
+    GAM_CTA(512, 16);
+  } else {
+    if (vecs <= 2048) GAM_CTA(512, 4);
+    GAM_CTA(1024, 16);
   }
-  return launch_status(cudaGetLastError());
+#undef GAM_WARPS
+#undef GAM_CTA
 }
 
 template <typename TX, typename TY, int V>
@@ -244,14 +286,14 @@ gam_status launch_g(const gam_residual_norm_args& p, int64_t per_gate, int sms, 
 template <typename TX, typename TY>
 gam_status launch(const gam_residual_norm_args& p, int64_t per_gate, int sms, cudaStream_t s) {
   constexpr int V = 16 / sizeof(TY);
-  auto rows_at = [&](size_t align_x, size_t align_y) {
+  auto bases = [&](size_t align_x, size_t align_y) {
     return aligned(p.x, align_x) && aligned(p.x_out, align_x) && aligned(p.y, align_y) && aligned(p.u, align_y) &&
            aligned(p.gate, align_y);
   };
   const int64_t strides[5] = {p.x_stride, p.y_stride, p.x_out_stride, p.u_stride, p.gate_stride};
-  bool wide = p.d % V == 0 && rows_at(16, 16) && aligned(p.layer_scale, 16) && aligned(p.post_weight, 16) &&
+  bool wide = p.d % V == 0 && bases(16, 16) && aligned(p.layer_scale, 16) && aligned(p.post_weight, 16) &&
               aligned(p.post_bias, 16) && aligned(p.pre_weight, 16) && aligned(p.pre_bias, 16);
-  bool pairs = rows_at(2 * sizeof(TX), 2 * sizeof(TY));
+  bool pairs = p.d < 16382 && bases(2 * sizeof(TX), 2 * sizeof(TY));  // 16 pairs to each of 512 threads, and a cut one
   for (int i = 0; i < (p.gate ? 5 : 4); ++i) {
     wide = wide && strides[i] % V == 0;
     pairs = pairs && (strides[i] - p.y_stride) % 2 == 0;
