@@ -20,9 +20,12 @@
 //
 // K is split over KW warps of a CTA (1 .. 16, a power of two) such that the tiles
 // times KW about fill the GPU's SMs with 16 warps each; the partial sums meet in
-// shared memory and are added in a fixed order.
+// shared memory and are added in a fixed order.  With few tiles and a long K it is
+// split over a cluster of CTAs too, whose sums the first adds in order.
 //
 // fp32 x is held as three bf16 parts (8 + 8 + 8 bits: exact), each with its own MMA.
+#include <cooperative_groups.h>
+
 #include <algorithm>
 
 #include "stream_ops.cuh"
@@ -30,6 +33,8 @@
 namespace gam {
 namespace ops {
 namespace {
+
+namespace cg = cooperative_groups;
 
 constexpr int kWarps = 16, kStages = 3, kStageBytes = 2048;
 constexpr int kRingBytes = kWarps * kStages * kStageBytes;
@@ -47,42 +52,77 @@ struct Elem<float> {
   static constexpr int parts = 3;
 };
 
+// c <- a b + (FIRST ? 0 : c)
+#define GAM_MMA(T)                                                                                                    \
+  if constexpr (FIRST)                                                                                                \
+    asm("mma.sync.aligned.m16n8k16.row.col.f32." T "." T ".f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "       \
+                 "{%10,%10,%10,%10};"                                                                                 \
+                 : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])                                                     \
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));                           \
+  else                                                                                                                \
+    asm("mma.sync.aligned.m16n8k16.row.col.f32." T "." T ".f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "       \
+                 "{%0,%1,%2,%3};"                                                                                     \
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])                                                     \
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1))
+template <bool FIRST>
 __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1, __half) {
-  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-               : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-               : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  GAM_MMA("f16");
 }
+template <bool FIRST>
 __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1, bf16) {
-  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-               : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-               : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  GAM_MMA("bf16");
 }
+#undef GAM_MMA
 
 // The 8 weights of a word as four pairs.  fp16: 1024 + u and, from the nibbles left
 // in place 4 bits up, 1024 + 16 u are exact, and so is the fused subtraction.
 // bf16: 128 + u is exact; the pairs are 2^-9 q there, so that a group's sum of the
-// largest finite x stays finite (64 * 7 < 2^9), and the scale takes 2^9 back.
-__device__ __forceinline__ void unpack8(uint32_t w, uint32_t (&p)[4], __half) {
-  const uint32_t w8 = w >> 8;
-  const uint32_t r[4] = {(w & 0x000F000Fu) | 0x64006400u, (w & 0x00F000F0u) | 0x64006400u,
-                         (w8 & 0x000F000Fu) | 0x64006400u, (w8 & 0x00F000F0u) | 0x64006400u};
-  const __half2 one = __float2half2_rn(1.f), lo = __float2half2_rn(-1032.f);
-  const __half2 six = __float2half2_rn(0.0625f), hi = __float2half2_rn(-72.f);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const __half2 v = *reinterpret_cast<const __half2*>(&r[i]);
-    const __half2 q = (i & 1) ? __hfma2(v, six, hi) : __hfma2(v, one, lo);
-    p[i] = *reinterpret_cast<const uint32_t*>(&q);
-  }
+// largest finite x stays finite (64 * 7 < 2^9), and the last step takes 2^9 back.
+// (a & mask) | magic in one instruction: both constants stay in registers.
+__device__ __forceinline__ uint32_t and_or(uint32_t a, uint32_t mask, uint32_t magic) {
+  uint32_t r;
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(a), "r"(mask), "r"(magic));
+  return r;
 }
-__device__ __forceinline__ void unpack8(uint32_t w, uint32_t (&p)[4], bf16) {
-  const __nv_bfloat162 f = __float2bfloat162_rn(0.001953125f), c = __float2bfloat162_rn(-136.f * 0.001953125f);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const uint32_t r = ((w >> (4 * i)) & 0x000F000Fu) | 0x43004300u;
-    const __nv_bfloat162 q = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&r), f, c);
-    p[i] = *reinterpret_cast<const uint32_t*>(&q);
+__device__ __forceinline__ uint32_t fma_pair(uint32_t a, uint32_t b, uint32_t c, __half) {
+  uint32_t r;
+  asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
+  return r;
+}
+__device__ __forceinline__ uint32_t fma_pair(uint32_t a, uint32_t b, uint32_t c, bf16) {
+  uint32_t r;
+  asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
+  return r;
+}
+// The constants of unpack8 (made once: an instruction takes one as an immediate at most).
+template <typename M>
+struct UnpackConst;
+template <>
+struct UnpackConst<__half> {
+  uint32_t lo, hi, magic, one, minus1032, sixteenth, minus72;
+  __device__ __forceinline__ UnpackConst()
+      : lo(0x000F000Fu), hi(0x00F000F0u), magic(0x64006400u), one(0x3C003C00u), minus1032(0xE408E408u),
+        sixteenth(0x2C002C00u), minus72(0xD480D480u) {
+    asm volatile("" : "+r"(lo), "+r"(hi), "+r"(magic));
   }
+};
+template <>
+struct UnpackConst<bf16> {
+  uint32_t lo, magic, scale, shift;  // 2^-9 and -136 * 2^-9
+  __device__ __forceinline__ UnpackConst() : lo(0x000F000Fu), magic(0x43004300u), scale(0x3B003B00u), shift(0xBE88BE88u) {
+    asm volatile("" : "+r"(lo), "+r"(magic));
+  }
+};
+__device__ __forceinline__ void unpack8(uint32_t w, uint32_t (&p)[4], const UnpackConst<__half>& k) {
+  const uint32_t w8 = w >> 8;
+  p[0] = fma_pair(and_or(w, k.lo, k.magic), k.one, k.minus1032, __half());
+  p[1] = fma_pair(and_or(w, k.hi, k.magic), k.sixteenth, k.minus72, __half());
+  p[2] = fma_pair(and_or(w8, k.lo, k.magic), k.one, k.minus1032, __half());
+  p[3] = fma_pair(and_or(w8, k.hi, k.magic), k.sixteenth, k.minus72, __half());
+}
+__device__ __forceinline__ void unpack8(uint32_t w, uint32_t (&p)[4], const UnpackConst<bf16>& k) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) p[i] = fma_pair(and_or(w >> (4 * i), k.lo, k.magic), k.scale, k.shift, bf16());
 }
 template <typename M>
 constexpr float kUnpackScale = 1.f;
@@ -112,6 +152,17 @@ __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_grou
 template <int N>
 __device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
+__device__ __forceinline__ uint2 lds8(uint32_t at) {
+  uint2 v;
+  asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(at) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint4 lds16(uint32_t at) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at) : "memory");
+  return v;
+}
+
 struct LinearArgs {
   const void* x;
   const uint8_t* packed;
@@ -121,9 +172,77 @@ struct LinearArgs {
   int64_t ldx, ldy;
   int act, rows, n, groups;   // groups = k / 64
   int kw;                     // warps that share a tile's K
+  int per;                    // groups of a stage: 4, 2 or 1
   int chunk;                  // groups of x held in shared memory at a time
   int wide;                   // x rows are 16-byte aligned
 };
+
+// Elements lo .. hi of the chunk from element k0 of x's rows on, to shared memory in parts of type M; asynchronous where no
+// conversion is needed.  The warps share the rows evenly.
+template <typename T>
+__device__ __forceinline__ void stage_x(const LinearArgs& p, uint8_t* xs, int xrow, int64_t k0, int lo, int hi) {
+  if (hi <= lo) return;
+  const int ke = hi - lo;
+  constexpr int PARTS = Elem<T>::parts;
+  const int xpart = p.rows * xrow;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  int per_row = 1;                                       // warps to a row
+  while (per_row * 2 * p.rows <= kWarps) per_row *= 2;
+  const int first = (warp % per_row) * 32 + lane, step = per_row * 32;
+  for (int r = warp / per_row; r < p.rows; r += kWarps / per_row) {
+    const T* src = (const T*)p.x + r * p.ldx + k0 + lo;
+    uint8_t* dst = xs + r * xrow + lo * 2;
+    if (p.wide) {
+      constexpr int V = 16 / sizeof(T), U = 4;
+      const int vecs = ke / V;
+      if constexpr (PARTS == 1) {
+        const char* from = reinterpret_cast<const char*>(src) + first * 16;
+        uint32_t to = (uint32_t)__cvta_generic_to_shared(dst) + first * 16;
+#pragma unroll 4
+        for (int v = first; v < vecs; v += step, from += step * 16, to += step * 16) cp_async16(to, from);
+      } else {
+        for (int v0 = first; v0 < vecs; v0 += U * step) {
+          Raw<T, V> in[U];
+#pragma unroll
+          for (int u = 0; u < U; ++u) in[u].load(src + min(v0 + u * step, vecs - 1) * V);
+#pragma unroll
+          for (int u = 0; u < U; ++u) {
+            const int v = min(v0 + u * step, vecs - 1);  // the last one again, with the same values
+            bf16 q[V][3];
+#pragma unroll
+            for (int j = 0; j < V; ++j) split(in[u].get(j), q[j]);
+#pragma unroll
+            for (int h = 0; h < 3; ++h) {
+              Vec<bf16, V> o;
+#pragma unroll
+              for (int j = 0; j < V; ++j) o.v[j] = q[j][h];
+              *reinterpret_cast<Vec<bf16, V>*>(dst + h * xpart + v * V * 2) = o;
+            }
+          }
+        }
+      }
+    } else {
+      constexpr int U = 8;
+      for (int v0 = first; v0 < ke; v0 += U * step) {
+        Raw<T, 1> in[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) in[u].load(src + min(v0 + u * step, ke - 1));
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const int v = min(v0 + u * step, ke - 1);
+          if constexpr (PARTS == 1) {
+            *reinterpret_cast<unsigned short*>(dst + v * 2) = (unsigned short)in[u].w[0];
+          } else {
+            bf16 q[3];
+            split(in[u].get(0), q);
+#pragma unroll
+            for (int h = 0; h < 3; ++h) *reinterpret_cast<bf16*>(dst + h * xpart + v * 2) = q[h];
+          }
+        }
+      }
+    }
+  }
+}
 
 // MT: 8-row tiles of x
 template <typename T, int MT>
@@ -131,139 +250,135 @@ __global__ void __launch_bounds__(kWarps * 32, 1) quant_linear_kernel(const Line
   using M = typename Elem<T>::M;
   constexpr int PARTS = Elem<T>::parts;
   extern __shared__ __align__(128) uint8_t smem[];
+  cg::cluster_group cluster = cg::this_cluster();
+  const int R = cluster.num_blocks(), rank = cluster.block_rank();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   uint8_t* ring = smem + warp * kStages * kStageBytes;
-  const uint32_t ring_u = (uint32_t)__cvta_generic_to_shared(ring);
   uint8_t* xs = smem + kRingBytes;
   const int xrow = p.chunk * 128 + 16;                  // bytes of a row of one part
   const int xpart = p.rows * xrow;
   const int kw = p.kw, per_cta = kWarps / kw, wk = warp & (kw - 1), wt = warp / kw;
   const int64_t row_bytes = (int64_t)p.groups * 32;
   const int tiles = (p.n + 15) / 16;
-  const T* x = (const T*)p.x;
-  bool staged = false;
+  const int k_lo = p.groups * rank / R, k_hi = p.groups * (rank + 1) / R;  // this CTA's groups
+  const bool one_chunk = k_hi - k_lo <= p.chunk;
+  // a lane copies 16 bytes of rows i 4 + lane / 8 of a stage; chunk c of row r lies in slot (c / 2) ^ (r & 3)
+  const int cr = lane >> 3, cc = lane & 7;
+  const uint32_t copy_to = (uint32_t)__cvta_generic_to_shared(ring) + cr * 128 + ((((cc >> 1) ^ cr) << 1) | (cc & 1)) * 16;
+  // columns of x behind the last row repeat row 0: they only reach outputs that are dropped
+  uint32_t xf[MT];
+#pragma unroll
+  for (int m = 0; m < MT; ++m)
+    xf[m] = (uint32_t)__cvta_generic_to_shared(xs) + (m * 8 + g < p.rows ? m * 8 + g : 0) * xrow + t * 32;
+  uint32_t frag[4];                                      // group G of the first stage
+#pragma unroll
+  for (int G = 0; G < 4; ++G) frag[G] = (uint32_t)__cvta_generic_to_shared(ring) + g * 128 + t * 8 + (G ^ (g & 3)) * 32;
 
-  for (int tb = blockIdx.x * per_cta; tb < tiles; tb += gridDim.x * per_cta) {
+  const UnpackConst<M> consts;
+  bool staged = false;
+  for (int tb = (blockIdx.x / R) * per_cta; tb < tiles; tb += (gridDim.x / R) * per_cta) {
     const int tile = tb + wt, o0 = tile * 16;
     const bool live = tile < tiles;
-    float acc[MT][4] = {};
-    for (int c0 = 0; c0 < p.groups; c0 += p.chunk) {
-      const int cg = min(p.chunk, p.groups - c0);
-      const int s0 = cg * wk / kw, s1 = live ? cg * (wk + 1) / kw : s0;   // this warp's groups of the chunk
-      const int stages = (s1 - s0 + 3) >> 2;
-      uint32_t sc[kStages];                              // scales of rows g and g + 8, group t of a stage
-      auto issue = [&](int st, uint32_t& sreg) {
-        if (st < stages) {
-          const int gb = c0 + s0 + st * 4, ng = min(4, s1 - s0 - st * 4);
-          const uint32_t dst = ring_u + (st % kStages) * kStageBytes;
+    const uint8_t* src[4];                               // rows past n are the last one again; dropped below
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int r = i * 4 + (lane >> 3), c = lane & 7;
-            if ((c >> 1) < ng)
-              cp_async16(dst + r * 128 + ((((c >> 1) ^ (r & 3)) << 1) | (c & 1)) * 16,
-                         p.packed + min(o0 + r, p.n - 1) * row_bytes + (int64_t)gb * 32 + c * 16);
-          }
-          const int gt = gb + min(t, ng - 1);
-          const __half a = p.scale[(int64_t)min(o0 + g, p.n - 1) * p.groups + gt];
-          const __half b = p.scale[(int64_t)min(o0 + g + 8, p.n - 1) * p.groups + gt];
-          const __half2 ab = __halves2half2(a, b);
-          sreg = *reinterpret_cast<const uint32_t*>(&ab);
+    for (int i = 0; i < 4; ++i) src[i] = p.packed + min(o0 + i * 4 + cr, p.n - 1) * row_bytes + cc * 16;
+    const __half* sa = p.scale + (int64_t)min(o0 + g, p.n - 1) * p.groups + t;
+    const __half* sb = p.scale + (int64_t)min(o0 + g + 8, p.n - 1) * p.groups + t;
+    float acc[MT][4] = {};
+    for (int c0 = k_lo; c0 < k_hi; c0 += p.chunk) {
+      const int held = min(p.chunk, k_hi - c0);
+      // stage st of this warp: groups (st kw + wk) per .. of the chunk, so that the warps go through K together
+      const int per = p.per, round = kw * per, stages = (held + round - 1) / round;
+      uint32_t sca[kStages], scb[kStages];               // scales of rows g and g + 8, group t of a stage (their bits)
+      // stage by stage: the sources move on with it
+      const uint8_t* from[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) from[i] = src[i] + (int64_t)(c0 + wk * per) * 32;
+      const __half *from_a = sa + c0 + wk * per, *from_b = sb + c0 + wk * per;
+      int todo = live ? held - wk * per : 0;             // groups from the next stage to issue on
+      auto issue = [&](int slot, uint32_t& s_a, uint32_t& s_b) {
+        const int ng = min(per, todo);
+        if ((cc >> 1) < ng)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) cp_async16(copy_to + slot * kStageBytes + i * 512, from[i]);
+        if (t < ng) {
+          s_a = *reinterpret_cast<const unsigned short*>(from_a);
+          s_b = *reinterpret_cast<const unsigned short*>(from_b);
         }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) from[i] += round * 32;
+        from_a += round;
+        from_b += round;
+        todo -= round;
         cp_commit();                                     // an empty group keeps the count
       };
+      if (!staged) __syncthreads();                      // the previous chunk of x is read
 #pragma unroll
-      for (int i = 0; i < kStages - 1; ++i) issue(i, sc[i]);
+      for (int i = 0; i < kStages - 1; ++i) issue(i, sca[i], scb[i]);
       if (!staged) {
-        __syncthreads();                                 // the previous chunk of x is read
-        const int ke = cg * 64;                          // elements of a row in this chunk
-        if (p.wide) {
-          constexpr int V = 16 / sizeof(T);
-          const int vecs = ke / V;
-          for (int i = threadIdx.x; i < p.rows * vecs; i += kWarps * 32) {
-            const int r = i / vecs, v = i % vecs;
-            const Vec<T, V> in = *reinterpret_cast<const Vec<T, V>*>(x + r * p.ldx + (int64_t)c0 * 64 + v * V);
-            if constexpr (PARTS == 1) {
-              *reinterpret_cast<Vec<T, V>*>(xs + r * xrow + v * 16) = in;
-            } else {
-              Vec<bf16, V> o[3];
-#pragma unroll
-              for (int j = 0; j < V; ++j) {
-                bf16 q[3];
-                split(in.v[j], q);
-                o[0].v[j] = q[0], o[1].v[j] = q[1], o[2].v[j] = q[2];
-              }
-#pragma unroll
-              for (int q = 0; q < 3; ++q) *reinterpret_cast<Vec<bf16, V>*>(xs + q * xpart + r * xrow + v * V * 2) = o[q];
-            }
-          }
-        } else {
-          for (int i = threadIdx.x; i < p.rows * ke; i += kWarps * 32) {
-            const int r = i / ke, v = i % ke;
-            const T in = x[r * p.ldx + (int64_t)c0 * 64 + v];
-            if constexpr (PARTS == 1) {
-              *reinterpret_cast<T*>(xs + r * xrow + v * 2) = in;
-            } else {
-              bf16 q[3];
-              split(in, q);
-#pragma unroll
-              for (int j = 0; j < 3; ++j) *reinterpret_cast<bf16*>(xs + j * xpart + r * xrow + v * 2) = q[j];
-            }
-          }
-        }
-        __syncthreads();
-        staged = p.chunk >= p.groups;                    // all of x stays for the following tiles
+        // the x of the first rounds, then the rest, which comes while those are worked on
+        const int head = min(held, (stages + 3) / 4 * round);
+        stage_x<T>(p, xs, xrow, (int64_t)c0 * 64, 0, head * 64);
+        cp_commit();
+        stage_x<T>(p, xs, xrow, (int64_t)c0 * 64, head * 64, held * 64);
+        cp_commit();
       }
-      // columns of x behind the last row repeat row 0: they only reach outputs that are dropped
-      const uint8_t* xf[MT];
+      // group G of a stage: its weights from at_w on, its x at_x behind the rows' starts
+      auto group = [&](uint32_t at_w, uint32_t at_x, int G, uint32_t s_a, uint32_t s_b) {
+        const uint2 wa = lds8(at_w), wb = lds8(at_w + 8 * 128);
+        s_a = __shfl_sync(0xffffffffu, s_a, (lane & 28) | G);
+        s_b = __shfl_sync(0xffffffffu, s_b, (lane & 28) | G);
+        float c[MT][4];
 #pragma unroll
-      for (int m = 0; m < MT; ++m) xf[m] = xs + (m * 8 + g < p.rows ? m * 8 + g : 0) * xrow + t * 32;
+        for (int h = 0; h < 2; ++h) {
+          uint32_t pa[4], pb[4];
+          unpack8(h ? wa.y : wa.x, pa, consts);
+          unpack8(h ? wb.y : wb.x, pb, consts);
+          const uint32_t a0[4] = {pa[0], pb[0], pa[1], pb[1]}, a1[4] = {pa[2], pb[2], pa[3], pb[3]};
+#pragma unroll
+          for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int q = 0; q < PARTS; ++q) {
+              const uint4 b = lds16(xf[m] + at_x + q * xpart + h * 16);
+              if (h == 0 && q == 0) mma16816<true>(c[m], a0, b.x, b.y, M());
+              else mma16816<false>(c[m], a0, b.x, b.y, M());
+              mma16816<false>(c[m], a1, b.z, b.w, M());
+            }
+        }
+        const float fa = __half2float(__ushort_as_half((unsigned short)s_a)), fb = __half2float(__ushort_as_half((unsigned short)s_b));
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+          acc[m][0] = fmaf(fa, c[m][0], acc[m][0]);
+          acc[m][1] = fmaf(fa, c[m][1], acc[m][1]);
+          acc[m][2] = fmaf(fb, c[m][2], acc[m][2]);
+          acc[m][3] = fmaf(fb, c[m][3], acc[m][3]);
+        }
+      };
       for (int st0 = 0; st0 < stages; st0 += kStages) {
 #pragma unroll
         for (int u = 0; u < kStages; ++u) {
           const int st = st0 + u;
           if (st >= stages) break;
-          cp_wait<kStages - 2>();
-          __syncwarp();                                  // every lane's copies of this stage are in; the slot before it is free
-          const uint32_t scales = sc[u];
-          issue(st + kStages - 1, sc[(u + kStages - 1) % kStages]);
-          const uint8_t* sw = ring + u * kStageBytes + g * 128 + t * 8;
-          const int gl = s0 + st * 4, ng = min(4, s1 - gl);
+          cp_wait<kStages - 2>();                        // at stage 0 of a new chunk: all but the rest of x
+          if (!staged && (st == 0 || st == (stages + 3) / 4)) __syncthreads();
+          else __syncwarp();                             // every lane's copies of this stage are in; the slot before it is free
+          const uint32_t s_a = sca[u], s_b = scb[u];
+          constexpr int kNext = kStages - 1;
+          issue((u + kNext) % kStages, sca[(u + kNext) % kStages], scb[(u + kNext) % kStages]);
+          const int gl = st * round + wk * per, ng = live ? min(per, held - gl) : 0;
+          if (ng == 4) {
 #pragma unroll
-          for (int G = 0; G < 4; ++G) {
-            if (G >= ng) break;
-            const uint2 wa = *reinterpret_cast<const uint2*>(sw + ((G ^ (g & 3)) * 32));
-            const uint2 wb = *reinterpret_cast<const uint2*>(sw + 8 * 128 + ((G ^ (g & 3)) * 32));
-            const uint32_t s2 = __shfl_sync(0xffffffffu, scales, (lane & 28) | G);
-            const float2 s = __half22float2(*reinterpret_cast<const __half2*>(&s2));
-            const float sa = s.x * kUnpackScale<M>, sb = s.y * kUnpackScale<M>;
-            float c[MT][4] = {};
+            for (int G = 0; G < 4; ++G) group(frag[G] + u * kStageBytes, (gl + G) * 128, G, s_a, s_b);
+          } else {
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              uint32_t pa[4], pb[4];
-              unpack8(h ? wa.y : wa.x, pa, M());
-              unpack8(h ? wb.y : wb.x, pb, M());
-              const uint32_t a0[4] = {pa[0], pb[0], pa[1], pb[1]}, a1[4] = {pa[2], pb[2], pa[3], pb[3]};
-#pragma unroll
-              for (int m = 0; m < MT; ++m)
-#pragma unroll
-                for (int q = 0; q < PARTS; ++q) {
-                  const uint4 b = *reinterpret_cast<const uint4*>(xf[m] + q * xpart + (gl + G) * 128 + h * 16);
-                  mma16816(c[m], a0, b.x, b.y, M());
-                  mma16816(c[m], a1, b.z, b.w, M());
-                }
-            }
-#pragma unroll
-            for (int m = 0; m < MT; ++m) {
-              acc[m][0] = fmaf(sa, c[m][0], acc[m][0]);
-              acc[m][1] = fmaf(sa, c[m][1], acc[m][1]);
-              acc[m][2] = fmaf(sb, c[m][2], acc[m][2]);
-              acc[m][3] = fmaf(sb, c[m][3], acc[m][3]);
-            }
+            for (int G = 0; G < 3; ++G)
+              if (G < ng) group(frag[G] + u * kStageBytes, (gl + G) * 128, G, s_a, s_b);
           }
         }
       }
       cp_wait<0>();
       __syncwarp();
+      staged = one_chunk;                                // all of x stays for the following tiles
     }
     // partial sums [warp][x row][16 outputs] over the idle ring: 64 rows at most, 4 KB a warp
     float* part = reinterpret_cast<float*>(ring);
@@ -272,12 +387,31 @@ __global__ void __launch_bounds__(kWarps * 32, 1) quant_linear_kernel(const Line
 #pragma unroll
       for (int e = 0; e < 4; ++e) part[(m * 8 + 2 * t + (e & 1)) * 16 + g + (e >> 1) * 8] = acc[m][e];
     __syncthreads();
-    const int outs = p.rows * 16;
-    for (int i = threadIdx.x; i < per_cta * outs; i += kWarps * 32) {
-      const int wi = i / outs, r = i % outs, m = r >> 4, o = (tb + wi) * 16 + (r & 15);
-      if (o >= p.n) continue;
+    // output i: value i % 16 of tile i / 16 % per_cta of row m (per_cta is a power of two)
+    const int outs = per_cta * 16 * p.rows, shift = __ffs(per_cta) + 3;
+    auto sum = [&](int i) {                              // over the tile's warps, in order
+      const int wi = (i >> 4) & (per_cta - 1), at = (i >> shift) * 16 + (i & 15);
       float v = 0.f;
-      for (int k = 0; k < kw; ++k) v += reinterpret_cast<float*>(smem + (wi * kw + k) * kStages * kStageBytes)[r];
+      for (int k = 0; k < kw; ++k) v += reinterpret_cast<float*>(smem + (wi * kw + k) * kStages * kStageBytes)[at];
+      return v;
+    };
+    if (R > 1) {
+      // to the first CTA, which adds the pieces of K in order: over the x it no longer reads (one tile to a CTA here)
+      float* join = reinterpret_cast<float*>(xs);
+      cluster.sync();
+      if (rank > 0) {
+        float* to = cluster.map_shared_rank(join, 0) + (rank - 1) * outs;
+        for (int i = threadIdx.x; i < outs; i += kWarps * 32) to[i] = sum(i);
+      }
+      cluster.sync();
+      if (rank > 0) return;
+    }
+    for (int i = threadIdx.x; i < outs; i += kWarps * 32) {
+      const int m = i >> shift, o = (tb * 16) + (i & (per_cta * 16 - 1));
+      if (o >= p.n) continue;
+      float v = sum(i);
+      for (int k = 1; k < R; ++k) v += reinterpret_cast<float*>(xs)[(k - 1) * outs + i];
+      v *= kUnpackScale<M>;
       if (p.bias) v += p.bias[o];
       ((T*)p.y)[m * p.ldy + o] = from_f<T>(p.act == GAM_ACT_SWISH ? swish_f(v) : v);
     }
@@ -291,23 +425,228 @@ gam_status launch_mt(LinearArgs p, int sms, cudaStream_t s) {
   const int tiles = (p.n + 15) / 16;
   p.kw = 1;
   while (p.kw < kWarps && p.kw * 2 <= p.groups && (int64_t)tiles * p.kw * 2 <= (int64_t)sms * kWarps) p.kw *= 2;
-  // all of x when it fits, else chunks of a multiple of 4 kw groups if possible, so that the warps' shares are even
+  // Few tiles and a long K: K over a cluster of R CTAs too, while each warp keeps 2 groups.
+  int R = 1;
+  if (p.kw == kWarps)
+    while (R < 8 && tiles * R * 2 <= sms && R * 2 * kWarps * 2 <= p.groups) R *= 2;
+  const int per_cta = kWarps / p.kw, own = (p.groups + R - 1) / R;
+  p.per = own >= 4 * p.kw ? 4 : own >= 2 * p.kw ? 2 : 1;
+  // all of a CTA's x when it fits, else chunks of a multiple of 4 kw groups if possible, so that the warps' shares are even
   const int most = (kXBytes / (p.rows * PARTS) - 16) / 128;
-  p.chunk = std::min(p.groups, most);
-  if (p.chunk < p.groups && p.chunk > 4 * p.kw) p.chunk = p.chunk / (4 * p.kw) * (4 * p.kw);
-  const int smem = kRingBytes + p.rows * PARTS * (p.chunk * 128 + 16);
+  p.chunk = std::min(own, most);
+  if (p.chunk < own && p.chunk > 4 * p.kw) p.chunk = p.chunk / (4 * p.kw) * (4 * p.kw);
+  const int x_bytes = std::max(p.rows * PARTS * (p.chunk * 128 + 16), (R - 1) * per_cta * p.rows * 16 * 4);
   auto kernel = quant_linear_kernel<T, MT>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
   if (e != cudaSuccess) return launch_status(e);
-  const int per_cta = kWarps / p.kw;
-  const int grid = std::min((tiles + per_cta - 1) / per_cta, sms);
-  kernel<<<grid, kWarps * 32, smem, s>>>(p);
-  return launch_status(cudaGetLastError());
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(R > 1 ? tiles * R : std::min((tiles + per_cta - 1) / per_cta, sms));
+  cfg.blockDim = dim3(kWarps * 32);
+  cfg.dynamicSmemBytes = kRingBytes + x_bytes;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = R;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = R > 1 ? 1 : 0;
+  return launch_status(cudaLaunchKernelEx(&cfg, kernel, p));
+}
+
+// ---- few rows or few weights ----
+// One or two 8-column tiles of x make few enough fragments that a warp reads them where they lie (L2 holds
+// x), so nothing is staged: a CTA of 8 warps takes one tile of 16 outputs and 8 MT rows, its warps every 8th
+// group of K, each with the weights and x of its next groups on their way.  The call's time is then one trip
+// to memory for a short K, and several CTAs to an SM keep the weight stream going for a long one.
+constexpr int kThinWarps = 8;
+
+template <typename T, int MT>
+struct ThinGroup {               // a lane's part of a group, as it lies in memory
+  uint2 w[2];                    // 16 weights of rows g and g + 8 of the tile
+  uint32_t s[2];                 // their scales' bits
+  uint32_t x[MT][16 * sizeof(T) / 4];
+};
+
+template <typename T, int MT>
+__global__ void __launch_bounds__(kThinWarps * 32, 3) quant_linear_thin_kernel(const LinearArgs p) {
+  using M = typename Elem<T>::M;
+  constexpr int PARTS = Elem<T>::parts, U = MT == 1 && PARTS == 1 ? 2 : 1;
+  __shared__ float part[kThinWarps][8 * MT][16];
+  extern __shared__ float join[];                        // [rank - 1][rows][16], in a cluster
+  cg::cluster_group cluster = cg::this_cluster();
+  const int R = cluster.num_blocks(), rank = cluster.block_rank();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const int o0 = (blockIdx.x / R) * 16, m0 = blockIdx.y * 8 * MT, rows = min(8 * MT, p.rows - m0);
+  const int k_lo = p.groups * rank / R, k_hi = p.groups * (rank + 1) / R;
+  const UnpackConst<M> consts;
+  // bases of this lane's rows (past the last: another one, dropped below)
+  const int64_t row_bytes = (int64_t)p.groups * 32;
+  const uint8_t* w[2];
+  const __half* sc[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int64_t o = min(o0 + h * 8 + g, p.n - 1);
+    w[h] = p.packed + o * row_bytes + t * 8;
+    sc[h] = p.scale + o * p.groups;
+  }
+  const T* x[MT];
+#pragma unroll
+  for (int m = 0; m < MT; ++m) x[m] = (const T*)p.x + (m0 + (m * 8 + g < rows ? m * 8 + g : 0)) * p.ldx + t * 16;
+  auto fetch = [&](ThinGroup<T, MT>& q, int k) {
+    k = min(k, k_hi - 1);                                // beyond the end the last group again, not used
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      q.w[h] = __ldg(reinterpret_cast<const uint2*>(w[h] + (int64_t)k * 32));
+      q.s[h] = *reinterpret_cast<const unsigned short*>(sc[h] + k);
+    }
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+      const T* from = x[m] + (int64_t)k * 64;
+      if (p.wide) {
+#pragma unroll
+        for (int i = 0; i < (int)sizeof(T); ++i) {
+          const uint4 v = reinterpret_cast<const uint4*>(from)[i];
+          q.x[m][4 * i] = v.x, q.x[m][4 * i + 1] = v.y, q.x[m][4 * i + 2] = v.z, q.x[m][4 * i + 3] = v.w;
+        }
+      } else if constexpr (sizeof(T) == 4) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) q.x[m][i] = reinterpret_cast<const uint32_t*>(from)[i];
+      } else {
+        const unsigned short* u = reinterpret_cast<const unsigned short*>(from);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) q.x[m][i] = u[2 * i] | (uint32_t)u[2 * i + 1] << 16;
+      }
+    }
+  };
+  float acc[MT][4] = {};
+  auto use = [&](const ThinGroup<T, MT>& q) {
+    uint32_t a[4][4];                                    // the group's four 16 x 16 pieces
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      uint32_t pa[4], pb[4];
+      unpack8(h ? q.w[0].y : q.w[0].x, pa, consts);
+      unpack8(h ? q.w[1].y : q.w[1].x, pb, consts);
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        a[2 * h + i][0] = pa[2 * i], a[2 * h + i][1] = pb[2 * i], a[2 * h + i][2] = pa[2 * i + 1], a[2 * h + i][3] = pb[2 * i + 1];
+    }
+    const float fa = __half2float(__ushort_as_half((unsigned short)q.s[0]));
+    const float fb = __half2float(__ushort_as_half((unsigned short)q.s[1]));
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+      float c[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        uint32_t b[PARTS][2];                            // pairs of consecutive values in each part
+        if constexpr (PARTS == 1) {
+          b[0][0] = q.x[m][2 * i], b[0][1] = q.x[m][2 * i + 1];
+        } else {
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            bf16 lo[3], hi[3];
+            split(__uint_as_float(q.x[m][4 * i + 2 * j]), lo);
+            split(__uint_as_float(q.x[m][4 * i + 2 * j + 1]), hi);
+#pragma unroll
+            for (int h = 0; h < 3; ++h) {
+              const __nv_bfloat162 v(lo[h], hi[h]);
+              b[h][j] = *reinterpret_cast<const uint32_t*>(&v);
+            }
+          }
+        }
+#pragma unroll
+        for (int e = 0; e < PARTS; ++e) {
+          if (i == 0 && e == 0) mma16816<true>(c, a[i], b[e][0], b[e][1], M());
+          else mma16816<false>(c, a[i], b[e][0], b[e][1], M());
+        }
+      }
+      acc[m][0] = fmaf(fa, c[0], acc[m][0]);
+      acc[m][1] = fmaf(fa, c[1], acc[m][1]);
+      acc[m][2] = fmaf(fb, c[2], acc[m][2]);
+      acc[m][3] = fmaf(fb, c[3], acc[m][3]);
+    }
+  };
+  ThinGroup<T, MT> now[U];
+  int k = k_lo + warp;
+  if (k < k_hi) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) fetch(now[u], k + u * kThinWarps);
+  }
+  while (k < k_hi) {
+    ThinGroup<T, MT> next[U];
+    if (k + U * kThinWarps < k_hi) {
+#pragma unroll
+      for (int u = 0; u < U; ++u) fetch(next[u], k + (U + u) * kThinWarps);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (k + u * kThinWarps < k_hi) use(now[u]);
+#pragma unroll
+    for (int u = 0; u < U; ++u) now[u] = next[u];
+    k += U * kThinWarps;
+  }
+#pragma unroll
+  for (int m = 0; m < MT; ++m)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) part[warp][m * 8 + 2 * t + (e & 1)][g + (e >> 1) * 8] = acc[m][e];
+  __syncthreads();
+  const int outs = rows * 16;
+  auto sum = [&](int i) {                                // over the warps, in order
+    float v = 0.f;
+#pragma unroll
+    for (int q = 0; q < kThinWarps; ++q) v += (&part[q][0][0])[i];
+    return v;
+  };
+  if (R > 1) {
+    // to the first CTA, which adds the pieces of K in order
+    cluster.sync();
+    if (rank > 0) {
+      float* to = cluster.map_shared_rank(join, 0) + (rank - 1) * outs;
+      for (int i = threadIdx.x; i < outs; i += kThinWarps * 32) to[i] = sum(i);
+    }
+    cluster.sync();
+    if (rank > 0) return;
+  }
+  for (int i = threadIdx.x; i < outs; i += kThinWarps * 32) {
+    const int m = m0 + i / 16, o = o0 + i % 16;
+    if (o >= p.n) continue;
+    float v = sum(i);
+    for (int q = 1; q < R; ++q) v += join[(q - 1) * outs + i];
+    v *= kUnpackScale<M>;
+    if (p.bias) v += p.bias[o];
+    ((T*)p.y)[m * p.ldy + o] = from_f<T>(p.act == GAM_ACT_SWISH ? swish_f(v) : v);
+  }
+}
+
+template <typename T, int MT>
+gam_status launch_thin(const LinearArgs& p, int sms, cudaStream_t s) {
+  const int tiles = (p.n + 15) / 16, blocks = (p.rows + 8 * MT - 1) / (8 * MT);
+  // few tiles and a long K: K over a cluster of R CTAs too, while each warp keeps 2 groups
+  int R = 1;
+  while (R < 8 && tiles * blocks * R * 2 <= sms * 2 && p.groups >= R * 2 * kThinWarps * 2) R *= 2;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(tiles * R, blocks);
+  cfg.blockDim = dim3(kThinWarps * 32);
+  cfg.dynamicSmemBytes = (R - 1) * std::min(p.rows, 8 * MT) * 16 * sizeof(float);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = R;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = R > 1 ? 1 : 0;
+  return launch_status(cudaLaunchKernelEx(&cfg, quant_linear_thin_kernel<T, MT>, p));
 }
 
 template <typename T>
 gam_status launch(const LinearArgs& p, int sms, cudaStream_t s) {
-  if (p.rows <= 8) return launch_mt<T, 1>(p, sms, s);
+  const int64_t weights = (int64_t)p.n * p.groups * 64;
+  if constexpr (Elem<T>::parts == 1) {
+    if (p.rows <= 8) return launch_thin<T, 1>(p, sms, s);
+    if (weights <= (32 << 20)) return launch_thin<T, 2>(p, sms, s);
+  } else {
+    if (weights <= (8 << 20)) return launch_thin<T, 1>(p, sms, s);  // splitting x again for every tile
+    if (p.rows <= 8) return launch_mt<T, 1>(p, sms, s);
+  }
   if (p.rows <= 16) return launch_mt<T, 2>(p, sms, s);
   if (p.rows <= 32) return launch_mt<T, 4>(p, sms, s);
   return launch_mt<T, 8>(p, sms, s);
@@ -356,7 +695,7 @@ extern "C" gam_status gam_quant_linear(const void* x, int dtype, int64_t ldx, co
     if (x == y) return op_fail(GAM_ERR_INVALID_ARG, "y must not be x");
     int sms = 0;
     if (gam_status st = check_device(&sms)) return st;
-    const LinearArgs p{x,   packed, static_cast<const __half*>(scale), bias, y, ldx, ldy, act, rows, n, k / 64, 1, 0,
+    const LinearArgs p{x,   packed, static_cast<const __half*>(scale), bias, y, ldx, ldy, act, rows, n, k / 64, 1, 4, 0,
                        aligned(x, 16) && (rows == 1 || ldx % (16 / es) == 0)};
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (dtype == GAM_DTYPE_F32) return launch<float>(p, sms, s);

@@ -677,7 +677,7 @@ gam_status launch_scan(const gam_scan_args& p, int sms, cudaStream_t s) {
   attr[0].val.clusterDim.x = R;
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = R > 1 ? 1 : 0;
   auto kernel = wide ? scan_kernel<T, S, L, CH, true> : scan_kernel<T, S, L, CH, false>;
   if (cfg.dynamicSmemBytes + CT * 8 + 64 > 48 * 1024) {  // with the static part
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)cfg.dynamicSmemBytes);
