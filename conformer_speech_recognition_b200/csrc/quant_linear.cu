@@ -5,23 +5,14 @@
 // The weights are read once and the rows are few, so the bound is the weight
 // stream (0.53 bytes per weight) and, close behind it, the instructions that turn
 // integers into an MMA operand.  A warp owns 16 outputs: mma.m16n8k16 with the
-// weights as the 16-row operand and up to 64 rows of x as 8-column tiles.  The
+// weights as the 16-row operand and rows of x as 8-column tiles.  The
 // integers are exact in both 16-bit types, so a group's sum is that of q x itself
 // and is scaled in fp32 by the group's scale.
 //
-// Weights reach a warp through its own ring of cp.async stages (16 rows x 128
-// bytes, 4 groups): fully coalesced, no barrier between warps, and enough bytes in
-// flight per SM to cover the memory's latency.  Inside a stage the 32-byte slot of
-// group G of row r is G ^ (r & 3), which makes the 8-byte fragment reads free of
-// bank conflicts.  The words' nibble order gives adjacent pairs by one shift and
-// mask.  A lane's 16 weights of a group are 16 consecutive k, so its fragments of x
-// are two 16-byte reads of a row in shared memory; rows are 16 bytes apart beyond
-// their length, again for the banks.
-//
-// K is split over KW warps of a CTA (1 .. 16, a power of two) such that the tiles
-// times KW about fill the GPU's SMs with 16 warps each; the partial sums meet in
-// shared memory and are added in a fixed order.  With few tiles and a long K it is
-// split over a cluster of CTAs too, whose sums the first adds in order.
+// The words' nibble order gives adjacent pairs by one shift and mask, and a lane's 16
+// weights of a group are 16 consecutive k, so its fragments of x are 16 consecutive
+// values of a row.  K is split over the warps of a CTA, and over a cluster of CTAs when
+// there are few tiles; partial sums are added in a fixed order.
 //
 // fp32 x is held as three bf16 parts (8 + 8 + 8 bits: exact), each with its own MMA.
 #include <cooperative_groups.h>
@@ -35,11 +26,6 @@ namespace ops {
 namespace {
 
 namespace cg = cooperative_groups;
-
-constexpr int kWarps = 16, kStages = 3, kStageBytes = 2048;
-constexpr int kRingBytes = kWarps * kStages * kStageBytes;
-constexpr int kMaxSmem = 227 * 1024;
-constexpr int kXBytes = kMaxSmem - kRingBytes;   // for x
 
 template <typename T>
 struct Elem {                  // how x enters the MMA: type and number of parts
@@ -145,13 +131,229 @@ __device__ __forceinline__ void split(float v, bf16 (&p)[3]) {
   p[2] = __float2bfloat16_rn(r - b);
 }
 
+struct LinearArgs {
+  const void* x;
+  const uint8_t* packed;
+  const __half* scale;
+  const float* bias;
+  void* y;
+  int64_t ldx, ldy;
+  int act, rows, n, groups;   // groups = k / 64
+  int wide;                   // x rows are 16-byte aligned
+  int kw, per, chunk;         // staged form: warps that share a tile's K, groups of a stage, groups of x held at a time
+};
+
+// ---- few rows or few weights ----
+// One or two 8-column tiles of x make few enough fragments that a warp reads them where they lie (L2 holds
+// x), so nothing is staged: a CTA of 8 warps takes one tile of 16 outputs and 8 MT rows, its warps every 8th
+// group of K, each with the weights and x of its next groups on their way.  The call's time is then one trip
+// to memory for a short K, and several CTAs to an SM keep the weight stream going for a long one.
+constexpr int kThinWarps = 8;
+
+template <typename T, int MT, int NT>
+struct ThinGroup {               // a lane's part of a group, as it lies in memory
+  uint2 w[NT][2];                // 16 weights of rows g and g + 8 of each tile
+  uint32_t s[NT][2];             // their scales' bits
+  uint32_t x[MT][16 * sizeof(T) / 4];
+};
+
+template <typename T, int MT, int NT>
+__global__ void __launch_bounds__(kThinWarps * 32, NT > 1 ? 2 : 3) quant_linear_thin_kernel(const LinearArgs p) {
+  using M = typename Elem<T>::M;
+  constexpr int PARTS = Elem<T>::parts, U = MT == 1 && NT == 1 && PARTS == 1 ? 2 : 1;
+  __shared__ float part[kThinWarps][8 * MT][NT * 16];
+  extern __shared__ float join[];                        // [rank - 1][rows][NT 16], in a cluster
+  cg::cluster_group cluster = cg::this_cluster();
+  const int R = cluster.num_blocks(), rank = cluster.block_rank();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const int o0 = (blockIdx.x / R) * NT * 16, m0 = blockIdx.y * 8 * MT, rows = min(8 * MT, p.rows - m0);
+  const int k_lo = p.groups * rank / R, k_hi = p.groups * (rank + 1) / R;
+  const UnpackConst<M> consts;
+  // bases of this lane's rows (past the last: another one, dropped below)
+  const int64_t row_bytes = (int64_t)p.groups * 32;
+  const uint8_t* w[NT][2];
+  const __half* sc[NT][2];
+#pragma unroll
+  for (int i = 0; i < NT; ++i)
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int64_t o = min(o0 + i * 16 + h * 8 + g, p.n - 1);
+      w[i][h] = p.packed + o * row_bytes + t * 8;
+      sc[i][h] = p.scale + o * p.groups;
+    }
+  const T* x[MT];
+#pragma unroll
+  for (int m = 0; m < MT; ++m) x[m] = (const T*)p.x + (m0 + (m * 8 + g < rows ? m * 8 + g : 0)) * p.ldx + t * 16;
+  auto fetch = [&](ThinGroup<T, MT, NT>& q, int k) {
+    k = min(k, k_hi - 1);                                // beyond the end the last group again, not used
+#pragma unroll
+    for (int i = 0; i < NT; ++i)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        q.w[i][h] = __ldg(reinterpret_cast<const uint2*>(w[i][h] + (int64_t)k * 32));
+        q.s[i][h] = *reinterpret_cast<const unsigned short*>(sc[i][h] + k);
+      }
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+      const T* from = x[m] + (int64_t)k * 64;
+      if (p.wide) {
+#pragma unroll
+        for (int i = 0; i < (int)sizeof(T); ++i) {
+          const uint4 v = reinterpret_cast<const uint4*>(from)[i];
+          q.x[m][4 * i] = v.x, q.x[m][4 * i + 1] = v.y, q.x[m][4 * i + 2] = v.z, q.x[m][4 * i + 3] = v.w;
+        }
+      } else if constexpr (sizeof(T) == 4) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) q.x[m][i] = reinterpret_cast<const uint32_t*>(from)[i];
+      } else {
+        const unsigned short* u = reinterpret_cast<const unsigned short*>(from);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) q.x[m][i] = u[2 * i] | (uint32_t)u[2 * i + 1] << 16;
+      }
+    }
+  };
+  float acc[NT][MT][4] = {};
+  auto use = [&](const ThinGroup<T, MT, NT>& q) {
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      uint32_t a[4][4];                                    // the group's four 16 x 16 pieces
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        uint32_t pa[4], pb[4];
+        unpack8(h ? q.w[n][0].y : q.w[n][0].x, pa, consts);
+        unpack8(h ? q.w[n][1].y : q.w[n][1].x, pb, consts);
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          a[2 * h + i][0] = pa[2 * i], a[2 * h + i][1] = pb[2 * i], a[2 * h + i][2] = pa[2 * i + 1], a[2 * h + i][3] = pb[2 * i + 1];
+    }
+      const float fa = __half2float(__ushort_as_half((unsigned short)q.s[n][0]));
+      const float fb = __half2float(__ushort_as_half((unsigned short)q.s[n][1]));
+#pragma unroll
+      for (int m = 0; m < MT; ++m) {
+        float c[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          uint32_t b[PARTS][2];                            // pairs of consecutive values in each part
+          if constexpr (PARTS == 1) {
+            b[0][0] = q.x[m][2 * i], b[0][1] = q.x[m][2 * i + 1];
+          } else {
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              bf16 lo[3], hi[3];
+              split(__uint_as_float(q.x[m][4 * i + 2 * j]), lo);
+              split(__uint_as_float(q.x[m][4 * i + 2 * j + 1]), hi);
+#pragma unroll
+              for (int h = 0; h < 3; ++h) {
+                const __nv_bfloat162 v(lo[h], hi[h]);
+                b[h][j] = *reinterpret_cast<const uint32_t*>(&v);
+              }
+            }
+          }
+#pragma unroll
+          for (int e = 0; e < PARTS; ++e) {
+            if (i == 0 && e == 0) mma16816<true>(c, a[i], b[e][0], b[e][1], M());
+            else mma16816<false>(c, a[i], b[e][0], b[e][1], M());
+          }
+        }
+        acc[n][m][0] = fmaf(fa, c[0], acc[n][m][0]);
+        acc[n][m][1] = fmaf(fa, c[1], acc[n][m][1]);
+        acc[n][m][2] = fmaf(fb, c[2], acc[n][m][2]);
+        acc[n][m][3] = fmaf(fb, c[3], acc[n][m][3]);
+    }
+    }
+  };
+  ThinGroup<T, MT, NT> now[U];
+  int k = k_lo + warp;
+  if (k < k_hi) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) fetch(now[u], k + u * kThinWarps);
+  }
+  while (k < k_hi) {
+    ThinGroup<T, MT, NT> next[U];
+    if (k + U * kThinWarps < k_hi) {
+#pragma unroll
+      for (int u = 0; u < U; ++u) fetch(next[u], k + (U + u) * kThinWarps);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (k + u * kThinWarps < k_hi) use(now[u]);
+#pragma unroll
+    for (int u = 0; u < U; ++u) now[u] = next[u];
+    k += U * kThinWarps;
+  }
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) part[warp][m * 8 + 2 * t + (e & 1)][n * 16 + g + (e >> 1) * 8] = acc[n][m][e];
+  __syncthreads();
+  const int outs = rows * NT * 16;
+  auto sum = [&](int i) {                                // over the warps, in order
+    float v = 0.f;
+#pragma unroll
+    for (int q = 0; q < kThinWarps; ++q) v += (&part[q][0][0])[i];
+    return v;
+  };
+  if (R > 1) {
+    // to the first CTA, which adds the pieces of K in order
+    cluster.sync();
+    if (rank > 0) {
+      float* to = cluster.map_shared_rank(join, 0) + (rank - 1) * outs;
+      for (int i = threadIdx.x; i < outs; i += kThinWarps * 32) to[i] = sum(i);
+    }
+    cluster.sync();
+    if (rank > 0) return;
+  }
+  for (int i = threadIdx.x; i < outs; i += kThinWarps * 32) {
+    const int m = m0 + i / (NT * 16), o = o0 + i % (NT * 16);
+    if (o >= p.n) continue;
+    float v = sum(i);
+    for (int q = 1; q < R; ++q) v += join[(q - 1) * outs + i];
+    v *= kUnpackScale<M>;
+    if (p.bias) v += p.bias[o];
+    ((T*)p.y)[m * p.ldy + o] = from_f<T>(p.act == GAM_ACT_SWISH ? swish_f(v) : v);
+  }
+}
+
+template <typename T, int MT, int NT>
+gam_status launch_thin(const LinearArgs& p, int sms, cudaStream_t s) {
+  const int tiles = (p.n + NT * 16 - 1) / (NT * 16), blocks = (p.rows + 8 * MT - 1) / (8 * MT);
+  // few tiles and a long K: K over a cluster of R CTAs too, while each warp keeps 2 groups
+  int R = 1;
+  while (R < 8 && tiles * blocks * R * 2 <= sms * 2 && p.groups >= R * 2 * kThinWarps * 2) R *= 2;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(tiles * R, blocks);
+  cfg.blockDim = dim3(kThinWarps * 32);
+  cfg.dynamicSmemBytes = (R - 1) * std::min(p.rows, 8 * MT) * NT * 16 * sizeof(float);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = R;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = R > 1 ? 1 : 0;
+  return launch_status(cudaLaunchKernelEx(&cfg, quant_linear_thin_kernel<T, MT, NT>, p));
+}
+
+// ---- many weights, fp32 ----
+// Splitting x into its parts takes more instructions than a tile's MMAs, so with many tiles it is done once per
+// CTA: the parts lie in shared memory (in chunks of K, rows 16 bytes apart beyond their length, for the banks)
+// and 16 warps read their fragments there.  Weights reach a warp through its own ring of cp.async stages (16 rows
+// x 128 bytes, 4 groups): fully coalesced, no barrier between warps.  Inside a stage the 32-byte slot of group G
+// of row r is G ^ (r & 3), which makes the 8-byte fragment reads free of bank conflicts.  K is split over KW warps
+// (1 .. 16, a power of two) such that the tiles times KW about fill the GPU's SMs with 16 warps each.
+constexpr int kWarps = 16, kStages = 3, kStageBytes = 2048;
+constexpr int kRingBytes = kWarps * kStages * kStageBytes;
+constexpr int kMaxSmem = 227 * 1024;
+constexpr int kXBytes = kMaxSmem - kRingBytes;   // for x
+
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
-
 __device__ __forceinline__ uint2 lds8(uint32_t at) {
   uint2 v;
   asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(at) : "memory");
@@ -163,81 +365,44 @@ __device__ __forceinline__ uint4 lds16(uint32_t at) {
   return v;
 }
 
-struct LinearArgs {
-  const void* x;
-  const uint8_t* packed;
-  const __half* scale;
-  const float* bias;
-  void* y;
-  int64_t ldx, ldy;
-  int act, rows, n, groups;   // groups = k / 64
-  int kw;                     // warps that share a tile's K
-  int per;                    // groups of a stage: 4, 2 or 1
-  int chunk;                  // groups of x held in shared memory at a time
-  int wide;                   // x rows are 16-byte aligned
-};
-
-// Elements lo .. hi of the chunk from element k0 of x's rows on, to shared memory in parts of type M; asynchronous where no
-// conversion is needed.  The warps share the rows evenly.
-template <typename T>
-__device__ __forceinline__ void stage_x(const LinearArgs& p, uint8_t* xs, int xrow, int64_t k0, int lo, int hi) {
-  if (hi <= lo) return;
-  const int ke = hi - lo;
-  constexpr int PARTS = Elem<T>::parts;
+// ke elements from k0 on of x's rows to shared memory in three bf16 parts.  The warps share the rows evenly.
+__device__ __forceinline__ void stage_x(const LinearArgs& p, uint8_t* xs, int xrow, int64_t k0, int ke) {
+  constexpr int U = 4;
   const int xpart = p.rows * xrow;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   int per_row = 1;                                       // warps to a row
   while (per_row * 2 * p.rows <= kWarps) per_row *= 2;
   const int first = (warp % per_row) * 32 + lane, step = per_row * 32;
+  // quads of values: the last one again beyond the end, with the same values
+  const int quads = ke / 4;
   for (int r = warp / per_row; r < p.rows; r += kWarps / per_row) {
-    const T* src = (const T*)p.x + r * p.ldx + k0 + lo;
-    uint8_t* dst = xs + r * xrow + lo * 2;
-    if (p.wide) {
-      constexpr int V = 16 / sizeof(T), U = 4;
-      const int vecs = ke / V;
-      if constexpr (PARTS == 1) {
-        const char* from = reinterpret_cast<const char*>(src) + first * 16;
-        uint32_t to = (uint32_t)__cvta_generic_to_shared(dst) + first * 16;
-#pragma unroll 4
-        for (int v = first; v < vecs; v += step, from += step * 16, to += step * 16) cp_async16(to, from);
-      } else {
-        for (int v0 = first; v0 < vecs; v0 += U * step) {
-          Raw<T, V> in[U];
+    const float* src = (const float*)p.x + r * p.ldx + k0;
+    uint8_t* dst = xs + r * xrow;
+    for (int v0 = first; v0 < quads; v0 += U * step) {
+      float in[U][4];
 #pragma unroll
-          for (int u = 0; u < U; ++u) in[u].load(src + min(v0 + u * step, vecs - 1) * V);
+      for (int u = 0; u < U; ++u) {
+        const float* from = src + min(v0 + u * step, quads - 1) * 4;
+        if (p.wide) {
+          const float4 q = *reinterpret_cast<const float4*>(from);
+          in[u][0] = q.x, in[u][1] = q.y, in[u][2] = q.z, in[u][3] = q.w;
+        } else {
 #pragma unroll
-          for (int u = 0; u < U; ++u) {
-            const int v = min(v0 + u * step, vecs - 1);  // the last one again, with the same values
-            bf16 q[V][3];
-#pragma unroll
-            for (int j = 0; j < V; ++j) split(in[u].get(j), q[j]);
-#pragma unroll
-            for (int h = 0; h < 3; ++h) {
-              Vec<bf16, V> o;
-#pragma unroll
-              for (int j = 0; j < V; ++j) o.v[j] = q[j][h];
-              *reinterpret_cast<Vec<bf16, V>*>(dst + h * xpart + v * V * 2) = o;
-            }
-          }
+          for (int j = 0; j < 4; ++j) in[u][j] = from[j];
         }
       }
-    } else {
-      constexpr int U = 8;
-      for (int v0 = first; v0 < ke; v0 += U * step) {
-        Raw<T, 1> in[U];
 #pragma unroll
-        for (int u = 0; u < U; ++u) in[u].load(src + min(v0 + u * step, ke - 1));
+      for (int u = 0; u < U; ++u) {
+        const int v = min(v0 + u * step, quads - 1);
+        bf16 q[4][3];
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-          const int v = min(v0 + u * step, ke - 1);
-          if constexpr (PARTS == 1) {
-            *reinterpret_cast<unsigned short*>(dst + v * 2) = (unsigned short)in[u].w[0];
-          } else {
-            bf16 q[3];
-            split(in[u].get(0), q);
+        for (int j = 0; j < 4; ++j) split(in[u][j], q[j]);
 #pragma unroll
-            for (int h = 0; h < 3; ++h) *reinterpret_cast<bf16*>(dst + h * xpart + v * 2) = q[h];
-          }
+        for (int h = 0; h < 3; ++h) {
+          Vec<bf16, 4> o;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) o.v[j] = q[j][h];
+          *reinterpret_cast<Vec<bf16, 4>*>(dst + h * xpart + v * 8) = o;
         }
       }
     }
@@ -245,13 +410,11 @@ __device__ __forceinline__ void stage_x(const LinearArgs& p, uint8_t* xs, int xr
 }
 
 // MT: 8-row tiles of x
-template <typename T, int MT>
-__global__ void __launch_bounds__(kWarps * 32, 1) quant_linear_kernel(const LinearArgs p) {
-  using M = typename Elem<T>::M;
-  constexpr int PARTS = Elem<T>::parts;
+template <int MT>
+__global__ void __launch_bounds__(kWarps * 32, 1) quant_linear_staged_kernel(const LinearArgs p) {
+  using M = bf16;
+  constexpr int PARTS = 3;
   extern __shared__ __align__(128) uint8_t smem[];
-  cg::cluster_group cluster = cg::this_cluster();
-  const int R = cluster.num_blocks(), rank = cluster.block_rank();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   uint8_t* ring = smem + warp * kStages * kStageBytes;
   uint8_t* xs = smem + kRingBytes;
@@ -260,8 +423,6 @@ __global__ void __launch_bounds__(kWarps * 32, 1) quant_linear_kernel(const Line
   const int kw = p.kw, per_cta = kWarps / kw, wk = warp & (kw - 1), wt = warp / kw;
   const int64_t row_bytes = (int64_t)p.groups * 32;
   const int tiles = (p.n + 15) / 16;
-  const int k_lo = p.groups * rank / R, k_hi = p.groups * (rank + 1) / R;  // this CTA's groups
-  const bool one_chunk = k_hi - k_lo <= p.chunk;
   // a lane copies 16 bytes of rows i 4 + lane / 8 of a stage; chunk c of row r lies in slot (c / 2) ^ (r & 3)
   const int cr = lane >> 3, cc = lane & 7;
   const uint32_t copy_to = (uint32_t)__cvta_generic_to_shared(ring) + cr * 128 + ((((cc >> 1) ^ cr) << 1) | (cc & 1)) * 16;
@@ -276,7 +437,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) quant_linear_kernel(const Line
 
   const UnpackConst<M> consts;
   bool staged = false;
-  for (int tb = (blockIdx.x / R) * per_cta; tb < tiles; tb += (gridDim.x / R) * per_cta) {
+  for (int tb = blockIdx.x * per_cta; tb < tiles; tb += gridDim.x * per_cta) {
     const int tile = tb + wt, o0 = tile * 16;
     const bool live = tile < tiles;
     const uint8_t* src[4];                               // rows past n are the last one again; dropped below
@@ -285,8 +446,8 @@ __global__ void __launch_bounds__(kWarps * 32, 1) quant_linear_kernel(const Line
     const __half* sa = p.scale + (int64_t)min(o0 + g, p.n - 1) * p.groups + t;
     const __half* sb = p.scale + (int64_t)min(o0 + g + 8, p.n - 1) * p.groups + t;
     float acc[MT][4] = {};
-    for (int c0 = k_lo; c0 < k_hi; c0 += p.chunk) {
-      const int held = min(p.chunk, k_hi - c0);
+    for (int c0 = 0; c0 < p.groups; c0 += p.chunk) {
+      const int held = min(p.chunk, p.groups - c0);
       // stage st of this warp: groups (st kw + wk) per .. of the chunk, so that the warps go through K together
       const int per = p.per, round = kw * per, stages = (held + round - 1) / round;
       uint32_t sca[kStages], scb[kStages];               // scales of rows g and g + 8, group t of a stage (their bits)
@@ -316,12 +477,9 @@ __global__ void __launch_bounds__(kWarps * 32, 1) quant_linear_kernel(const Line
 #pragma unroll
       for (int i = 0; i < kStages - 1; ++i) issue(i, sca[i], scb[i]);
       if (!staged) {
-        // the x of the first rounds, then the rest, which comes while those are worked on
-        const int head = min(held, (stages + 3) / 4 * round);
-        stage_x<T>(p, xs, xrow, (int64_t)c0 * 64, 0, head * 64);
-        cp_commit();
-        stage_x<T>(p, xs, xrow, (int64_t)c0 * 64, head * 64, held * 64);
-        cp_commit();
+        stage_x(p, xs, xrow, (int64_t)c0 * 64, held * 64);
+        __syncthreads();
+        staged = p.chunk >= p.groups;                    // all of x stays for the following tiles
       }
       // group G of a stage: its weights from at_w on, its x at_x behind the rows' starts
       auto group = [&](uint32_t at_w, uint32_t at_x, int G, uint32_t s_a, uint32_t s_b) {
@@ -359,9 +517,8 @@ __global__ void __launch_bounds__(kWarps * 32, 1) quant_linear_kernel(const Line
         for (int u = 0; u < kStages; ++u) {
           const int st = st0 + u;
           if (st >= stages) break;
-          cp_wait<kStages - 2>();                        // at stage 0 of a new chunk: all but the rest of x
-          if (!staged && (st == 0 || st == (stages + 3) / 4)) __syncthreads();
-          else __syncwarp();                             // every lane's copies of this stage are in; the slot before it is free
+          cp_wait<kStages - 2>();
+          __syncwarp();                                  // every lane's copies of this stage are in; the slot before it is free
           const uint32_t s_a = sca[u], s_b = scb[u];
           constexpr int kNext = kStages - 1;
           issue((u + kNext) % kStages, sca[(u + kNext) % kStages], scb[(u + kNext) % kStages]);
@@ -378,7 +535,6 @@ __global__ void __launch_bounds__(kWarps * 32, 1) quant_linear_kernel(const Line
       }
       cp_wait<0>();
       __syncwarp();
-      staged = one_chunk;                                // all of x stays for the following tiles
     }
     // partial sums [warp][x row][16 outputs] over the idle ring: 64 rows at most, 4 KB a warp
     float* part = reinterpret_cast<float*>(ring);
@@ -395,261 +551,54 @@ __global__ void __launch_bounds__(kWarps * 32, 1) quant_linear_kernel(const Line
       for (int k = 0; k < kw; ++k) v += reinterpret_cast<float*>(smem + (wi * kw + k) * kStages * kStageBytes)[at];
       return v;
     };
-    if (R > 1) {
-      // to the first CTA, which adds the pieces of K in order: over the x it no longer reads (one tile to a CTA here)
-      float* join = reinterpret_cast<float*>(xs);
-      cluster.sync();
-      if (rank > 0) {
-        float* to = cluster.map_shared_rank(join, 0) + (rank - 1) * outs;
-        for (int i = threadIdx.x; i < outs; i += kWarps * 32) to[i] = sum(i);
-      }
-      cluster.sync();
-      if (rank > 0) return;
-    }
     for (int i = threadIdx.x; i < outs; i += kWarps * 32) {
       const int m = i >> shift, o = (tb * 16) + (i & (per_cta * 16 - 1));
       if (o >= p.n) continue;
       float v = sum(i);
-      for (int k = 1; k < R; ++k) v += reinterpret_cast<float*>(xs)[(k - 1) * outs + i];
       v *= kUnpackScale<M>;
       if (p.bias) v += p.bias[o];
-      ((T*)p.y)[m * p.ldy + o] = from_f<T>(p.act == GAM_ACT_SWISH ? swish_f(v) : v);
+      ((float*)p.y)[m * p.ldy + o] = p.act == GAM_ACT_SWISH ? swish_f(v) : v;
     }
     __syncthreads();
   }
 }
 
-template <typename T, int MT>
-gam_status launch_mt(LinearArgs p, int sms, cudaStream_t s) {
-  constexpr int PARTS = Elem<T>::parts;
+template <int MT>
+gam_status launch_staged(LinearArgs p, int sms, cudaStream_t s) {
+  constexpr int PARTS = 3;
   const int tiles = (p.n + 15) / 16;
   p.kw = 1;
   while (p.kw < kWarps && p.kw * 2 <= p.groups && (int64_t)tiles * p.kw * 2 <= (int64_t)sms * kWarps) p.kw *= 2;
-  // Few tiles and a long K: K over a cluster of R CTAs too, while each warp keeps 2 groups.
-  int R = 1;
-  if (p.kw == kWarps)
-    while (R < 8 && tiles * R * 2 <= sms && R * 2 * kWarps * 2 <= p.groups) R *= 2;
-  const int per_cta = kWarps / p.kw, own = (p.groups + R - 1) / R;
-  p.per = own >= 4 * p.kw ? 4 : own >= 2 * p.kw ? 2 : 1;
-  // all of a CTA's x when it fits, else chunks of a multiple of 4 kw groups if possible, so that the warps' shares are even
-  const int most = (kXBytes / (p.rows * PARTS) - 16) / 128;
-  p.chunk = std::min(own, most);
-  if (p.chunk < own && p.chunk > 4 * p.kw) p.chunk = p.chunk / (4 * p.kw) * (4 * p.kw);
-  const int x_bytes = std::max(p.rows * PARTS * (p.chunk * 128 + 16), (R - 1) * per_cta * p.rows * 16 * 4);
-  auto kernel = quant_linear_kernel<T, MT>;
+  const int per_cta = kWarps / p.kw;
+  p.per = p.groups >= 4 * p.kw ? 4 : p.groups >= 2 * p.kw ? 2 : 1;
+  // all of x when it fits, else chunks of a multiple of 4 kw groups if possible, so that the warps' shares are even
+  p.chunk = std::min(p.groups, (kXBytes / (p.rows * PARTS) - 16) / 128);
+  if (p.chunk < p.groups && p.chunk > 4 * p.kw) p.chunk = p.chunk / (4 * p.kw) * (4 * p.kw);
+  auto kernel = quant_linear_staged_kernel<MT>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
   if (e != cudaSuccess) return launch_status(e);
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(R > 1 ? tiles * R : std::min((tiles + per_cta - 1) / per_cta, sms));
-  cfg.blockDim = dim3(kWarps * 32);
-  cfg.dynamicSmemBytes = kRingBytes + x_bytes;
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = R;
-  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = R > 1 ? 1 : 0;
-  return launch_status(cudaLaunchKernelEx(&cfg, kernel, p));
+  const int smem = kRingBytes + p.rows * PARTS * (p.chunk * 128 + 16);
+  kernel<<<std::min((tiles + per_cta - 1) / per_cta, sms), kWarps * 32, smem, s>>>(p);
+  return launch_status(cudaGetLastError());
 }
 
-// ---- few rows or few weights ----
-// One or two 8-column tiles of x make few enough fragments that a warp reads them where they lie (L2 holds
-// x), so nothing is staged: a CTA of 8 warps takes one tile of 16 outputs and 8 MT rows, its warps every 8th
-// group of K, each with the weights and x of its next groups on their way.  The call's time is then one trip
-// to memory for a short K, and several CTAs to an SM keep the weight stream going for a long one.
-constexpr int kThinWarps = 8;
-
-template <typename T, int MT>
-struct ThinGroup {               // a lane's part of a group, as it lies in memory
-  uint2 w[2];                    // 16 weights of rows g and g + 8 of the tile
-  uint32_t s[2];                 // their scales' bits
-  uint32_t x[MT][16 * sizeof(T) / 4];
-};
-
-template <typename T, int MT>
-__global__ void __launch_bounds__(kThinWarps * 32, 3) quant_linear_thin_kernel(const LinearArgs p) {
-  using M = typename Elem<T>::M;
-  constexpr int PARTS = Elem<T>::parts, U = MT == 1 && PARTS == 1 ? 2 : 1;
-  __shared__ float part[kThinWarps][8 * MT][16];
-  extern __shared__ float join[];                        // [rank - 1][rows][16], in a cluster
-  cg::cluster_group cluster = cg::this_cluster();
-  const int R = cluster.num_blocks(), rank = cluster.block_rank();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  const int o0 = (blockIdx.x / R) * 16, m0 = blockIdx.y * 8 * MT, rows = min(8 * MT, p.rows - m0);
-  const int k_lo = p.groups * rank / R, k_hi = p.groups * (rank + 1) / R;
-  const UnpackConst<M> consts;
-  // bases of this lane's rows (past the last: another one, dropped below)
-  const int64_t row_bytes = (int64_t)p.groups * 32;
-  const uint8_t* w[2];
-  const __half* sc[2];
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const int64_t o = min(o0 + h * 8 + g, p.n - 1);
-    w[h] = p.packed + o * row_bytes + t * 8;
-    sc[h] = p.scale + o * p.groups;
-  }
-  const T* x[MT];
-#pragma unroll
-  for (int m = 0; m < MT; ++m) x[m] = (const T*)p.x + (m0 + (m * 8 + g < rows ? m * 8 + g : 0)) * p.ldx + t * 16;
-  auto fetch = [&](ThinGroup<T, MT>& q, int k) {
-    k = min(k, k_hi - 1);                                // beyond the end the last group again, not used
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      q.w[h] = __ldg(reinterpret_cast<const uint2*>(w[h] + (int64_t)k * 32));
-      q.s[h] = *reinterpret_cast<const unsigned short*>(sc[h] + k);
-    }
-#pragma unroll
-    for (int m = 0; m < MT; ++m) {
-      const T* from = x[m] + (int64_t)k * 64;
-      if (p.wide) {
-#pragma unroll
-        for (int i = 0; i < (int)sizeof(T); ++i) {
-          const uint4 v = reinterpret_cast<const uint4*>(from)[i];
-          q.x[m][4 * i] = v.x, q.x[m][4 * i + 1] = v.y, q.x[m][4 * i + 2] = v.z, q.x[m][4 * i + 3] = v.w;
-        }
-      } else if constexpr (sizeof(T) == 4) {
-#pragma unroll
-        for (int i = 0; i < 16; ++i) q.x[m][i] = reinterpret_cast<const uint32_t*>(from)[i];
-      } else {
-        const unsigned short* u = reinterpret_cast<const unsigned short*>(from);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) q.x[m][i] = u[2 * i] | (uint32_t)u[2 * i + 1] << 16;
-      }
-    }
-  };
-  float acc[MT][4] = {};
-  auto use = [&](const ThinGroup<T, MT>& q) {
-    uint32_t a[4][4];                                    // the group's four 16 x 16 pieces
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      uint32_t pa[4], pb[4];
-      unpack8(h ? q.w[0].y : q.w[0].x, pa, consts);
-      unpack8(h ? q.w[1].y : q.w[1].x, pb, consts);
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-        a[2 * h + i][0] = pa[2 * i], a[2 * h + i][1] = pb[2 * i], a[2 * h + i][2] = pa[2 * i + 1], a[2 * h + i][3] = pb[2 * i + 1];
-    }
-    const float fa = __half2float(__ushort_as_half((unsigned short)q.s[0]));
-    const float fb = __half2float(__ushort_as_half((unsigned short)q.s[1]));
-#pragma unroll
-    for (int m = 0; m < MT; ++m) {
-      float c[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        uint32_t b[PARTS][2];                            // pairs of consecutive values in each part
-        if constexpr (PARTS == 1) {
-          b[0][0] = q.x[m][2 * i], b[0][1] = q.x[m][2 * i + 1];
-        } else {
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            bf16 lo[3], hi[3];
-            split(__uint_as_float(q.x[m][4 * i + 2 * j]), lo);
-            split(__uint_as_float(q.x[m][4 * i + 2 * j + 1]), hi);
-#pragma unroll
-            for (int h = 0; h < 3; ++h) {
-              const __nv_bfloat162 v(lo[h], hi[h]);
-              b[h][j] = *reinterpret_cast<const uint32_t*>(&v);
-            }
-          }
-        }
-#pragma unroll
-        for (int e = 0; e < PARTS; ++e) {
-          if (i == 0 && e == 0) mma16816<true>(c, a[i], b[e][0], b[e][1], M());
-          else mma16816<false>(c, a[i], b[e][0], b[e][1], M());
-        }
-      }
-      acc[m][0] = fmaf(fa, c[0], acc[m][0]);
-      acc[m][1] = fmaf(fa, c[1], acc[m][1]);
-      acc[m][2] = fmaf(fb, c[2], acc[m][2]);
-      acc[m][3] = fmaf(fb, c[3], acc[m][3]);
-    }
-  };
-  ThinGroup<T, MT> now[U];
-  int k = k_lo + warp;
-  if (k < k_hi) {
-#pragma unroll
-    for (int u = 0; u < U; ++u) fetch(now[u], k + u * kThinWarps);
-  }
-  while (k < k_hi) {
-    ThinGroup<T, MT> next[U];
-    if (k + U * kThinWarps < k_hi) {
-#pragma unroll
-      for (int u = 0; u < U; ++u) fetch(next[u], k + (U + u) * kThinWarps);
-    }
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-      if (k + u * kThinWarps < k_hi) use(now[u]);
-#pragma unroll
-    for (int u = 0; u < U; ++u) now[u] = next[u];
-    k += U * kThinWarps;
-  }
-#pragma unroll
-  for (int m = 0; m < MT; ++m)
-#pragma unroll
-    for (int e = 0; e < 4; ++e) part[warp][m * 8 + 2 * t + (e & 1)][g + (e >> 1) * 8] = acc[m][e];
-  __syncthreads();
-  const int outs = rows * 16;
-  auto sum = [&](int i) {                                // over the warps, in order
-    float v = 0.f;
-#pragma unroll
-    for (int q = 0; q < kThinWarps; ++q) v += (&part[q][0][0])[i];
-    return v;
-  };
-  if (R > 1) {
-    // to the first CTA, which adds the pieces of K in order
-    cluster.sync();
-    if (rank > 0) {
-      float* to = cluster.map_shared_rank(join, 0) + (rank - 1) * outs;
-      for (int i = threadIdx.x; i < outs; i += kThinWarps * 32) to[i] = sum(i);
-    }
-    cluster.sync();
-    if (rank > 0) return;
-  }
-  for (int i = threadIdx.x; i < outs; i += kThinWarps * 32) {
-    const int m = m0 + i / 16, o = o0 + i % 16;
-    if (o >= p.n) continue;
-    float v = sum(i);
-    for (int q = 1; q < R; ++q) v += join[(q - 1) * outs + i];
-    v *= kUnpackScale<M>;
-    if (p.bias) v += p.bias[o];
-    ((T*)p.y)[m * p.ldy + o] = from_f<T>(p.act == GAM_ACT_SWISH ? swish_f(v) : v);
-  }
-}
-
-template <typename T, int MT>
-gam_status launch_thin(const LinearArgs& p, int sms, cudaStream_t s) {
-  const int tiles = (p.n + 15) / 16, blocks = (p.rows + 8 * MT - 1) / (8 * MT);
-  // few tiles and a long K: K over a cluster of R CTAs too, while each warp keeps 2 groups
-  int R = 1;
-  while (R < 8 && tiles * blocks * R * 2 <= sms * 2 && p.groups >= R * 2 * kThinWarps * 2) R *= 2;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(tiles * R, blocks);
-  cfg.blockDim = dim3(kThinWarps * 32);
-  cfg.dynamicSmemBytes = (R - 1) * std::min(p.rows, 8 * MT) * 16 * sizeof(float);
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = R;
-  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = R > 1 ? 1 : 0;
-  return launch_status(cudaLaunchKernelEx(&cfg, quant_linear_thin_kernel<T, MT>, p));
-}
-
+// Forms by size, measured in us (thin with one tile, thin with two, staged):
+//   16-bit, 16 x 16384 x 4096: 27.2, 19.5, 19.3; 30 x 3712 x 5888: 17.7, 11.6, 20.8; 16 x 4096 x 1024: 3.6, 3.5, 3.4
+//   16-bit, 2 x 4745 x 4224: 7.5, -, 9.4; 1 x 768 x 768: 2.4, -, 5.0
+//   fp32, 2 x 15083 x 3904: 36.7, 37.1, 20.3; 16 x 16384 x 4096: 77.7, 68.0, 43.1; 64 x 4096 x 4096: 76.2, 66.1, 173
+//   fp32, 7 x 6272 x 2496: 13.5, 14.9, 12.1; 5 x 1025 x 1024: 3.8, 4.9, 5.2
 template <typename T>
 gam_status launch(const LinearArgs& p, int sms, cudaStream_t s) {
   const int64_t weights = (int64_t)p.n * p.groups * 64;
   if constexpr (Elem<T>::parts == 1) {
-    if (p.rows <= 8) return launch_thin<T, 1>(p, sms, s);
-    if (weights <= (32 << 20)) return launch_thin<T, 2>(p, sms, s);
+    if (p.rows <= 8) return launch_thin<T, 1, 1>(p, sms, s);
+    return p.n < 2048 ? launch_thin<T, 2, 1>(p, sms, s) : launch_thin<T, 2, 2>(p, sms, s);
   } else {
-    if (weights <= (8 << 20)) return launch_thin<T, 1>(p, sms, s);  // splitting x again for every tile
-    if (p.rows <= 8) return launch_mt<T, 1>(p, sms, s);
+    if (weights <= (8 << 20)) return launch_thin<T, 1, 1>(p, sms, s);
+    if (p.rows <= 8) return launch_staged<1>(p, sms, s);
+    if (p.rows <= 16) return launch_staged<2>(p, sms, s);
+    return launch_thin<T, 1, 2>(p, sms, s);
   }
-  if (p.rows <= 16) return launch_mt<T, 2>(p, sms, s);
-  if (p.rows <= 32) return launch_mt<T, 4>(p, sms, s);
-  return launch_mt<T, 8>(p, sms, s);
 }
 
 }  // namespace
@@ -695,8 +644,8 @@ extern "C" gam_status gam_quant_linear(const void* x, int dtype, int64_t ldx, co
     if (x == y) return op_fail(GAM_ERR_INVALID_ARG, "y must not be x");
     int sms = 0;
     if (gam_status st = check_device(&sms)) return st;
-    const LinearArgs p{x,   packed, static_cast<const __half*>(scale), bias, y, ldx, ldy, act, rows, n, k / 64, 1, 4, 0,
-                       aligned(x, 16) && (rows == 1 || ldx % (16 / es) == 0)};
+    const LinearArgs p{x,   packed, static_cast<const __half*>(scale), bias, y, ldx, ldy, act, rows, n, k / 64,
+                       aligned(x, 16) && (rows == 1 || ldx % (16 / es) == 0), 1, 4, 0};
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (dtype == GAM_DTYPE_F32) return launch<float>(p, sms, s);
     if (dtype == GAM_DTYPE_F16) return launch<__half>(p, sms, s);

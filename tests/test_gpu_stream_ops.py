@@ -79,7 +79,8 @@ def linear_check(y, xf, q, scale, b, act, dtype):
     (1, 1, 64, "none", False), (1, 768, 768, "none", True), (2, 17, 192, "swish", True), (5, 1025, 1024, "none", True),
     (7, 31, 64, "none", False), (8, 256, 512, "swish", False), (9, 100, 320, "none", True), (16, 512, 2048, "swish", True),
     (17, 48, 128, "none", False), (33, 130, 448, "swish", True), (64, 257, 4096, "none", True), (1, 4100, 4160, "none", False),
-    (3, 16, 16384, "none", True)])
+    (3, 16, 16384, "none", True), (11, 2100, 4160, "none", False), (16, 600, 16384, "swish", True),
+    (20, 2101, 4160, "none", True), (17, 4801, 128, "swish", True), (9, 33, 8192, "none", False)])
 def test_linear(dtype, rows, n, k, act, bias):
     x, xf, q, scale, b = linear_inputs(rows * 1000 + n + k, rows, n, k, dtype, bias)
     y = gam.gam_quant_linear(x, dev(gam.gam_quant_linear_pack(q)), dev(scale), bias=None if b is None else dev(b), act=act)
@@ -91,7 +92,11 @@ def test_linear(dtype, rows, n, k, act, bias):
 def test_linear_strided_rows_and_untouched_memory(dtype):
     """x and out inside larger buffers at an odd offset: nothing beside out's rows changes."""
     torch = _torch()
-    rows, n, k = 6, 37, 192
+    linear_strided(torch, 6, 37, 192, dtype)
+    linear_strided(torch, 10, 2051, 4160, dtype)   # weights enough for every form
+
+
+def linear_strided(torch, rows, n, k, dtype):
     x, xf, q, scale, b = linear_inputs(11, rows, n, k, dtype, True)
     xb = torch.full((rows, k + 9), float("nan"), dtype=x.dtype, device="cuda")
     xv = xb[:, 3:3 + k]
