@@ -23,7 +23,7 @@
 // state.  Twice the exponentials, R times the SMs.
 //
 // Few frames (step_kernel, t_max <= 4): the states are the traffic; a thread holds
-// 4 states (one 16-byte access) and keeps them in registers over the frames.
+// 4 states of two channels (16-byte accesses) and keeps them in registers over the frames.
 #include <cooperative_groups.h>
 
 #include <algorithm>
@@ -564,85 +564,126 @@ scan_kernel(const gam_scan_args p, const int sms, const bool pair) {
   }
 }
 
-// A few frames: L lanes of 4 states to a channel, neighbouring lanes on neighbouring memory.
-template <typename T, int L, bool VEC>
+// A few frames: L lanes of 4 states to a channel, neighbouring lanes on neighbouring memory;
+// a thread has two channels on their way at a time, 256 / L apart.
+template <typename T, int L, bool VEC, bool QUAD>
 __global__ void __launch_bounds__(256) step_kernel(const gam_scan_args p) {
-  constexpr int CT = 256 / L;
-  const int cblocks = (p.d + CT - 1) / CT;
+  constexpr int CT = 256 / L, CH = 2;
+  const int cblocks = (p.d + CT * CH - 1) / (CT * CH);
   const int cb = blockIdx.x % cblocks, b = blockIdx.x / cblocks;
-  const int part = threadIdx.x % L, c0 = cb * CT + threadIdx.x / L;
-  const bool on = c0 < p.d;
-  const int c = on ? c0 : p.d - 1;                   // lanes past the last channel walk along, for the shuffles
+  const int part = threadIdx.x % L, c0 = cb * CT * CH + threadIdx.x / L;
   const int k0 = part * 4;
   const int len = length_of(p, b);
-  const int64_t at = ((int64_t)b * p.d + c) * p.n + k0;
-  float a[4] = {}, h[4] = {};
-  if constexpr (VEC) {                               // n a multiple of 4, 16-byte aligned
-    if (k0 < p.n) {
-      const float4 q = *reinterpret_cast<const float4*>(p.a + (int64_t)c * p.n + k0);
-      a[0] = q.x, a[1] = q.y, a[2] = q.z, a[3] = q.w;
-      if (p.state_in) {
-        const float4 w = *reinterpret_cast<const float4*>(p.state_in + at);
-        h[0] = w.x, h[1] = w.y, h[2] = w.z, h[3] = w.w;
+  float a[CH][4], h[CH][4], skip[CH], bias[CH];
+  int ch[CH];
+#pragma unroll
+  for (int j = 0; j < CH; ++j) {
+    ch[j] = min(c0 + j * CT, p.d - 1);               // lanes past the last channel walk along, for the shuffles
+    const float* pa = p.a + (int64_t)ch[j] * p.n + k0;
+    const float* ph = p.state_in ? p.state_in + ((int64_t)b * p.d + ch[j]) * p.n + k0 : nullptr;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) a[j][i] = h[j][i] = 0.f;
+    if constexpr (VEC) {                             // n a multiple of 4, 16-byte aligned
+      if (k0 < p.n) {
+        if (ph) {
+          const float4 w = *reinterpret_cast<const float4*>(ph);
+          h[j][0] = w.x, h[j][1] = w.y, h[j][2] = w.z, h[j][3] = w.w;
+        }
+        const float4 q = __ldg(reinterpret_cast<const float4*>(pa));
+        a[j][0] = q.x, a[j][1] = q.y, a[j][2] = q.z, a[j][3] = q.w;
       }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (k0 + i < p.n) {
+          if (ph) h[j][i] = ph[i];
+          a[j][i] = __ldg(pa + i);
+        }
     }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (k0 + i < p.n) {
-        a[i] = p.a[(int64_t)c * p.n + k0 + i];
-        if (p.state_in) h[i] = p.state_in[at + i];
-      }
+    skip[j] = p.d_skip ? __ldg(p.d_skip + ch[j]) : 0.f;
+    bias[j] = p.dt_bias ? __ldg(p.dt_bias + ch[j]) : 0.f;
   }
-#pragma unroll
-  for (int i = 0; i < 4; ++i) a[i] *= kLog2e;
-  const float skip = p.d_skip ? p.d_skip[c] : 0.f, bias = p.dt_bias ? p.dt_bias[c] : 0.f;
-  T* y = (T*)p.y + b * p.y_batch_stride + c;
+  const T* px = (const T*)p.x + b * p.x_batch_stride;
+  const T* pdt = (const T*)p.dt + b * p.dt_batch_stride;
+  const T* pz = p.z ? (const T*)p.z + b * p.z_batch_stride : nullptr;
+  const T* pb = (const T*)p.b + b * p.b_batch_stride + k0;
+  const T* pc = (const T*)p.c + b * p.c_batch_stride + k0;
+  T* y = (T*)p.y + b * p.y_batch_stride;
   for (int t = 0; t < len; ++t) {
-    const T* bb = (const T*)p.b + b * p.b_batch_stride + t * p.b_row_stride + k0;
-    const T* cc = (const T*)p.c + b * p.c_batch_stride + t * p.c_row_stride + k0;
-    const float xv = to_f(((const T*)p.x)[b * p.x_batch_stride + t * p.x_row_stride + c]);
-    float s = to_f(((const T*)p.dt)[b * p.dt_batch_stride + t * p.dt_row_stride + c]) + bias;
-    const float z = p.z ? to_f(((const T*)p.z)[b * p.z_batch_stride + t * p.z_row_stride + c]) : 0.f;
-    float bv[4], cv[4];
+    uint32_t ux[CH], ud[CH], uz[CH], ub[4], uc[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      bv[i] = k0 + i < p.n ? to_f(bb[i]) : 0.f;
-      cv[i] = k0 + i < p.n ? to_f(cc[i]) : 0.f;
+    for (int j = 0; j < CH; ++j) {
+      ud[j] = load_bits(pdt + t * p.dt_row_stride + ch[j]);
+      ux[j] = load_bits(px + t * p.x_row_stride + ch[j]);
+      uz[j] = pz ? load_bits(pz + t * p.z_row_stride + ch[j]) : 0;
     }
-    if (p.dt_softplus) s = softplus_f(s);
-    const float sx = s * xv;
-    float v = 0.f;
+    float bv[4] = {}, cv[4] = {};
+    if constexpr (QUAD) {                            // rows of b and c in whole quads, n a multiple of 4
+      if (k0 < p.n) {
+        const Vec<T, 4> q = *reinterpret_cast<const Vec<T, 4>*>(pb + t * p.b_row_stride);
+        const Vec<T, 4> r = *reinterpret_cast<const Vec<T, 4>*>(pc + t * p.c_row_stride);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      h[i] = fmaf(exp2_approx(s * a[i]), h[i], sx * bv[i]);
-      v = fmaf(cv[i], h[i], v);
+        for (int i = 0; i < 4; ++i) bv[i] = to_f(q.v[i]), cv[i] = to_f(r.v[i]);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        ub[i] = uc[i] = 0;
+        if (k0 + i < p.n) {
+          ub[i] = load_bits(pb + t * p.b_row_stride + i);
+          uc[i] = load_bits(pc + t * p.c_row_stride + i);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) bv[i] = from_bits<T>(ub[i]), cv[i] = from_bits<T>(uc[i]);
     }
+    float2 s = make_float2(from_bits<T>(ud[0]) + bias[0], from_bits<T>(ud[1]) + bias[1]);
+    if (p.dt_softplus) s = softplus2(s);
 #pragma unroll
-    for (int o = L / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    v = fmaf(skip, xv, v);
-    if (p.z) v *= gate_f(z);
-    if (on && part == 0) y[t * p.y_row_stride] = from_f<T>(v);
+    for (int j = 0; j < CH; ++j) {
+      const float st = j ? s.y : s.x, xv = from_bits<T>(ux[j]), sx = st * xv, e = st * kLog2e;
+      float v = 0.f;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        h[j][i] = fmaf(exp2_approx(e * a[j][i]), h[j][i], sx * bv[i]);
+        v = fmaf(cv[i], h[j][i], v);
+      }
+#pragma unroll
+      for (int o = L / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+      v = fmaf(skip[j], xv, v);
+      if (pz) v *= gate_f(from_bits<T>(uz[j]));
+      if (c0 + j * CT < p.d && part == 0) y[t * p.y_row_stride + ch[j]] = from_f<T>(v);
+    }
   }
-  if (on && part == 0)
-    for (int t = len; t < p.t_max; ++t) y[t * p.y_row_stride] = from_f<T>(0.f);
-  if (!on || !p.state_out) return;
-  if constexpr (VEC) {
-    if (k0 < p.n) *reinterpret_cast<float4*>(p.state_out + at) = make_float4(h[0], h[1], h[2], h[3]);
-  } else {
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (k0 + i < p.n) p.state_out[at + i] = h[i];
+  for (int j = 0; j < CH; ++j) {
+    if (c0 + j * CT >= p.d) continue;
+    if (part == 0)
+      for (int t = len; t < p.t_max; ++t) y[t * p.y_row_stride + ch[j]] = from_f<T>(0.f);
+    if (!p.state_out) continue;
+    float* ph = p.state_out + ((int64_t)b * p.d + ch[j]) * p.n + k0;
+    if constexpr (VEC) {
+      if (k0 < p.n) *reinterpret_cast<float4*>(ph) = make_float4(h[j][0], h[j][1], h[j][2], h[j][3]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (k0 + i < p.n) ph[i] = h[j][i];
+    }
   }
 }
 
 template <typename T, int L>
 gam_status launch_step(const gam_scan_args& p, cudaStream_t s) {
-  const int64_t grid = (int64_t)((p.d + 256 / L - 1) / (256 / L)) * p.batch;
+  const int64_t grid = (int64_t)((p.d + 512 / L - 1) / (512 / L)) * p.batch;
   if (grid > INT32_MAX) return op_fail(GAM_ERR_CAPACITY, "batch * d too large for one call");
+  const unsigned g = (unsigned)grid;
   const bool vec = p.n % 4 == 0 && aligned(p.a, 16) && aligned(p.state_in, 16) && aligned(p.state_out, 16);
-  if (vec) step_kernel<T, L, true><<<(unsigned)grid, 256, 0, s>>>(p);
-  else step_kernel<T, L, false><<<(unsigned)grid, 256, 0, s>>>(p);
+  constexpr size_t kQuad = 4 * sizeof(T);
+  const bool quad = p.n % 4 == 0 && aligned(p.b, kQuad) && aligned(p.c, kQuad) && p.b_batch_stride % 4 == 0 &&
+                    p.b_row_stride % 4 == 0 && p.c_batch_stride % 4 == 0 && p.c_row_stride % 4 == 0;
+  if (vec && quad) step_kernel<T, L, true, true><<<g, 256, 0, s>>>(p);
+  else if (vec) step_kernel<T, L, true, false><<<g, 256, 0, s>>>(p);
+  else step_kernel<T, L, false, false><<<g, 256, 0, s>>>(p);
   return launch_status(cudaGetLastError());
 }
 
