@@ -43,17 +43,22 @@ __device__ __forceinline__ float row_sum(float v, float (*red)[32], int& turn) {
 // A thread's part of a row: accesses j < NV of V columns from j G V + first on, first being
 // its own multiple of V less the phase (pairs).  G is known at compile time, so that an
 // access is one base register and a constant.  Only a pair can lie partly beside the row.
-template <int G, int V>
+// The first FULL accesses lie in the row for every thread (the row is long enough), but for
+// the column before the first.
+template <int G, int V, int FULL>
 struct Place {
   int first, d;
-  __device__ __forceinline__ bool on(int j, int i) const { return (unsigned)(first + j * G * V + i) < (unsigned)d; }
+  __device__ __forceinline__ bool on(int j, int i) const {
+    if (j < FULL) return V != 2 || j > 0 || i > 0 || first >= 0;
+    return (unsigned)(first + j * G * V + i) < (unsigned)d;
+  }
   __device__ __forceinline__ bool whole(int j) const { return on(j, 0) && (V != 2 || on(j, 1)); }
 };
 
 // The row's values; 0 for what lies beside it, which is not read.  Whole accesses first,
 // then the halves of cut pairs, so that nothing waits on the way.
-template <int G, int V, int NV, typename T>
-__device__ __forceinline__ void load_row(Raw<T, V> (&r)[NV], const T* row, const Place<G, V>& at) {
+template <int G, int V, int NV, int FULL, typename T>
+__device__ __forceinline__ void load_row(Raw<T, V> (&r)[NV], const T* row, const Place<G, V, FULL>& at) {
   const T* mine = row + at.first;
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
@@ -63,7 +68,7 @@ __device__ __forceinline__ void load_row(Raw<T, V> (&r)[NV], const T* row, const
   if constexpr (V == 2) {
 #pragma unroll
     for (int j = 0; j < NV; ++j)
-      if (at.on(j, 0) != at.on(j, 1)) {
+      if ((j == 0 || j >= FULL) && at.on(j, 0) != at.on(j, 1)) {
         const int i = at.on(j, 1);
         Raw<T, 1> one;
         one.load(mine + j * G * V + i);
@@ -72,8 +77,8 @@ __device__ __forceinline__ void load_row(Raw<T, V> (&r)[NV], const T* row, const
       }
   }
 }
-template <int G, int V, int NV, typename T>
-__device__ __forceinline__ void store_row(T* row, const Place<G, V>& at, const float (&v)[NV][V]) {
+template <int G, int V, int NV, int FULL, typename T>
+__device__ __forceinline__ void store_row(T* row, const Place<G, V, FULL>& at, const float (&v)[NV][V]) {
   T* mine = row + at.first;
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
@@ -89,8 +94,8 @@ __device__ __forceinline__ void store_row(T* row, const Place<G, V>& at, const f
   }
 }
 // Access j of a parameter vector [d]; 0 beside the row.
-template <int G, int V>
-__device__ __forceinline__ void load_param(float (&out)[V], const float* p, const Place<G, V>& at, int j) {
+template <int G, int V, int FULL>
+__device__ __forceinline__ void load_param(float (&out)[V], const float* p, const Place<G, V, FULL>& at, int j) {
   const float* mine = p + at.first + j * G * V;
 #pragma unroll
   for (int i = 0; i < V; ++i) out[i] = 0.f;
@@ -108,14 +113,14 @@ __device__ __forceinline__ void load_param(float (&out)[V], const float* p, cons
 }
 
 // v <- norm(v) over the row; v is 0 beside it, before and after.
-template <int G, int V, int NV>
+template <int G, int V, int NV, int FULL>
 __device__ __forceinline__ void norm_row(float (&v)[NV][V], bool layer, const float* w, const float* b, float eps,
-                                         const Place<G, V>& at, float (*red)[32], int& turn) {
+                                         const Place<G, V, FULL>& at, float (*red)[32], int& turn) {
   // one access a thread: its weights come while the row is summed
   float w0[V], b0[V];
   if constexpr (NV == 1) {
-    if (w) load_param<G, V>(w0, w, at, 0);
-    if (b) load_param<G, V>(b0, b, at, 0);
+    if (w) load_param<G, V, FULL>(w0, w, at, 0);
+    if (b) load_param<G, V, FULL>(b0, b, at, 0);
   }
   const float inv = 1.f / at.d;
   if (layer) {
@@ -143,14 +148,14 @@ __device__ __forceinline__ void norm_row(float (&v)[NV][V], bool layer, const fl
   if (w)
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      if constexpr (NV > 1) load_param<G, V>(w0, w, at, j);
+      if constexpr (NV > 1) load_param<G, V, FULL>(w0, w, at, j);
 #pragma unroll
       for (int i = 0; i < V; ++i) v[j][i] *= w0[i];
     }
   if (b)
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      if constexpr (NV > 1) load_param<G, V>(b0, b, at, j);
+      if constexpr (NV > 1) load_param<G, V, FULL>(b0, b, at, j);
 #pragma unroll
       for (int i = 0; i < V; ++i) v[j][i] += b0[i];
     }
@@ -158,7 +163,7 @@ __device__ __forceinline__ void norm_row(float (&v)[NV][V], bool layer, const fl
 
 constexpr int kWarps = 4;  // rows of a CTA at a time in the warp form
 
-template <typename TX, typename TY, int G, int V, int NV, bool GATE>
+template <typename TX, typename TY, int G, int V, int NV, int FULL, bool GATE>
 __global__ void __launch_bounds__(G == 32 ? 32 * kWarps : G, G == 32 ? (NV == 4 ? 3 : 5) : NV * V <= 12 ? 1024 / G : 1)
 residual_norm_kernel(const gam_residual_norm_args p, const int64_t per_gate) {
   constexpr bool WARP = G == 32;
@@ -168,14 +173,14 @@ residual_norm_kernel(const gam_residual_norm_args p, const int64_t per_gate) {
   const int own = (int)(WARP ? threadIdx.x & 31 : threadIdx.x) * V;
   const float* post_b = p.post_norm == GAM_NORM_LAYER ? p.post_bias : nullptr;
   const float* pre_b = p.pre_norm == GAM_NORM_LAYER ? p.pre_bias : nullptr;
-  Place<G, V> at{own, p.d};
+  Place<G, V, FULL> at{own, p.d};
   Raw<TX, V> rx[NV];
   Raw<TY, V> ry[NV], rg[GATE ? NV : 1];
   auto fetch = [&](int64_t r) {
     if constexpr (V == 2) at.first = own - ((int)(r * p.y_stride) & 1);
-    load_row<G, V, NV>(ry, (const TY*)p.y + r * p.y_stride, at);
-    load_row<G, V, NV>(rx, (const TX*)p.x + r * p.x_stride, at);
-    if constexpr (GATE) load_row<G, V, NV>(rg, (const TY*)p.gate + r / per_gate * p.gate_stride, at);
+    load_row<G, V, NV, FULL>(ry, (const TY*)p.y + r * p.y_stride, at);
+    load_row<G, V, NV, FULL>(rx, (const TX*)p.x + r * p.x_stride, at);
+    if constexpr (GATE) load_row<G, V, NV, FULL>(rg, (const TY*)p.gate + r / per_gate * p.gate_stride, at);
   };
   if (row >= p.rows) return;
   fetch(row);
@@ -190,10 +195,10 @@ residual_norm_kernel(const gam_residual_norm_args p, const int64_t per_gate) {
         x[j][i] = rx[j].get(i);
         if constexpr (GATE) g[j][i] = rg[j].get(i);
       }
-    const Place<G, V> here = at;
+    const Place<G, V, FULL> here = at;
     if (WARP && row + step < p.rows) fetch(row + step);
     if (p.post_norm)
-      norm_row<G, V, NV>(y, p.post_norm == GAM_NORM_LAYER, p.post_weight, post_b, p.eps, here, red, turn);
+      norm_row<G, V, NV, FULL>(y, p.post_norm == GAM_NORM_LAYER, p.post_weight, post_b, p.eps, here, red, turn);
     if constexpr (GATE) {
       auto gate = [&](auto act) {
 #pragma unroll
@@ -212,7 +217,7 @@ residual_norm_kernel(const gam_residual_norm_args p, const int64_t per_gate) {
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
         float ls[V];
-        load_param<G, V>(ls, p.layer_scale, here, j);
+        load_param<G, V, FULL>(ls, p.layer_scale, here, j);
 #pragma unroll
         for (int i = 0; i < V; ++i) y[j][i] *= ls[i];
       }
@@ -220,11 +225,11 @@ residual_norm_kernel(const gam_residual_norm_args p, const int64_t per_gate) {
     for (int j = 0; j < NV; ++j)
 #pragma unroll
       for (int i = 0; i < V; ++i) x[j][i] = fmaf(p.alpha, y[j][i], x[j][i]);
-    if (p.x_out) store_row<G, V, NV>((TX*)p.x_out + row * p.x_out_stride, here, x);
+    if (p.x_out) store_row<G, V, NV, FULL>((TX*)p.x_out + row * p.x_out_stride, here, x);
     if (p.u) {
       if (p.pre_norm)
-        norm_row<G, V, NV>(x, p.pre_norm == GAM_NORM_LAYER, p.pre_weight, pre_b, p.eps, here, red, turn);
-      store_row<G, V, NV>((TY*)p.u + row * p.u_stride, here, x);
+        norm_row<G, V, NV, FULL>(x, p.pre_norm == GAM_NORM_LAYER, p.pre_weight, pre_b, p.eps, here, red, turn);
+      store_row<G, V, NV, FULL>((TY*)p.u + row * p.u_stride, here, x);
     }
     row += step;
     if (!WARP || row >= p.rows) return;
@@ -244,35 +249,36 @@ gam_status launch_v(const gam_residual_norm_args& p, int64_t per_gate, int sms, 
     kernel<<<(unsigned)p.rows, threads, 0, s>>>(p, per_gate);
     return launch_status(cudaGetLastError());
   };
-#define GAM_WARPS(NV, PER_SM) return warps(residual_norm_kernel<TX, TY, 32, V, NV, GATE>, PER_SM)
-#define GAM_CTA(G, NV) return cta(residual_norm_kernel<TX, TY, G, V, NV, GATE>, G)
+#define GAM_WARPS(NV, FULL, PER_SM) return warps(residual_norm_kernel<TX, TY, 32, V, NV, FULL, GATE>, PER_SM)
+#define GAM_CTA(G, NV, FULL) return cta(residual_norm_kernel<TX, TY, G, V, NV, FULL, GATE>, G)
   // Rows enough for 8 warps to an SM: a warp holds a row, up to 4 accesses to a lane; else a CTA holds it.
   const bool many = p.rows >= 8 * sms;
+  // (accesses, of which whole in every row of this branch's lengths; vecs counts one pair more than a row may have)
   if constexpr (V > 2) {
-    if (vecs <= 32) GAM_WARPS(1, 8);
-    if (vecs <= 64 && many) GAM_WARPS(2, 5);
-    if (vecs <= 128 && many) GAM_WARPS(4, 3);
-    if (vecs <= 128) GAM_CTA(128, 1);
-    if (vecs <= 256) GAM_CTA(256, 1);
-    if (vecs <= 512) GAM_CTA(512, 1);
-    if (vecs <= 768) GAM_CTA(256, 3);
-    if (vecs <= 1024) GAM_CTA(512, 2);
+    if (vecs <= 32) GAM_WARPS(1, 0, 8);
+    if (vecs <= 64 && many) GAM_WARPS(2, 1, 5);
+    if (vecs <= 128 && many) GAM_WARPS(4, 2, 3);
+    if (vecs <= 128) GAM_CTA(128, 1, 0);
+    if (vecs <= 256) GAM_CTA(256, 1, 0);
+    if (vecs <= 512) GAM_CTA(512, 1, 0);
+    if (vecs <= 768) GAM_CTA(256, 3, 2);
+    if (vecs <= 1024) GAM_CTA(512, 2, 1);
     if constexpr (V == 4) {
-      if (vecs > 2048) GAM_CTA(512, 8);
+      if (vecs > 2048) GAM_CTA(512, 8, 4);
     }
-    GAM_CTA(512, 4);
+    GAM_CTA(512, 4, 2);
   } else if constexpr (V == 2) {
-    if (vecs <= 32) GAM_WARPS(1, 8);
-    if (vecs <= 128 && many) GAM_WARPS(4, 3);
-    if (vecs <= 384) GAM_CTA(128, 3);
-    if (vecs <= 768) GAM_CTA(256, 3);
-    if (vecs <= 1536) GAM_CTA(512, 3);
-    if (vecs <= 2560) GAM_CTA(512, 5);
-    if (vecs <= 4096) GAM_CTA(512, 8);
-    GAM_CTA(512, 16);
+    if (vecs <= 32) GAM_WARPS(1, 0, 8);
+    if (vecs <= 128 && many) GAM_WARPS(4, 0, 3);
+    if (vecs <= 384) GAM_CTA(128, 3, 0);
+    if (vecs <= 768) GAM_CTA(256, 3, 1);
+    if (vecs <= 1536) GAM_CTA(512, 3, 1);
+    if (vecs <= 2560) GAM_CTA(512, 5, 2);
+    if (vecs <= 4096) GAM_CTA(512, 8, 4);
+    GAM_CTA(512, 16, 7);
   } else {
-    if (vecs <= 2048) GAM_CTA(512, 4);
-    GAM_CTA(1024, 16);
+    if (vecs <= 2048) GAM_CTA(512, 4, 0);
+    GAM_CTA(1024, 16, 2);
   }
 #undef GAM_WARPS
 #undef GAM_CTA
