@@ -6,13 +6,15 @@
 // row of y and x in registers, so each is read once; all loads of a row are on
 // their way before the first is used, and a warp's next row while it works on
 // this one.  Statistics are two-pass in fp32 (mean, then the centred squares)
-// over those registers.  The bound is memory.
+// over those registers.  The bound is memory: 23968 rows of 1024 (fp32 residual, fp16
+// branch, 295 MB) in 59 us, 5.0 TB/s; a CTA to each of those rows 69 us.
 //
 // Accesses are 16 bytes where rows are 16-byte aligned.  Else they are pairs of
 // values: a row of odd offset starts with the second half of a pair, so pair i
 // holds columns 2 i - phase and the next, phase being the offset's last bit, and
 // every whole pair is aligned whatever the row.  Without that (arrays whose rows
-// differ in that bit) they are single values.
+// differ in that bit) they are single values.  2047 rows of 4099 in bf16 with a gate: 37 us
+// in pairs (2.3 TB/s; 21.6 M instructions at 2.3 a clock bound it), 79 us in single values.
 #include <algorithm>
 
 #include "stream_ops.cuh"

@@ -7,13 +7,22 @@
 // the fp32 multiply-adds; the bytes come far behind for 16 states and more.
 //
 // Frames in numbers (scan_kernel): a CTA takes 64 / L channels (or twice as many) of
-// one sequence; L neighbouring lanes share a channel and hold S states each in registers (S L
-// >= n; states past n have a = b = c = 0).  Time goes in tiles of 512 (frame,
-// channel) pairs, 8 neighbouring channels of a frame to a thread: it
-// fetches them one tile ahead in 16-byte accesses, forms s and s x once for the L
-// lanes, and later applies skip and gate to the y the lanes have left in shared
-// memory.  Inside a tile the lanes only read shared memory and their registers;
-// two states go through one packed fp32 instruction.
+// one sequence; L neighbouring lanes share a channel and hold S states each in
+// registers (S L >= n; states past n have a = b = c = 0).  Time goes in tiles of 512
+// (frame, channel) pairs.  A producer's share of a tile is 8 neighbouring channels of a
+// frame: it copies them ahead, forms s and s x once for the L lanes, and later applies
+// skip and gate to the y the lanes have left in shared memory.  Inside a tile the lanes
+// only read shared memory and their registers; two states go through one packed fp32
+// instruction.  Small calls, where a tile's latency counts, have producer warps beside the
+// lanes (2 x 4011 frames of 192 channels: 96 us without them, 63 with); in large calls a
+// thread does both, with two channels to a lane (32 x 390 frames of 2048 channels: 179 us,
+// with producers 249), which halves the reads of b and c.
+//
+// What it measured (16 states): 12.5 k frames of 2048 channels in 207 us, the special-function
+// pipe 57 % busy (exponentials and the gates' reciprocals) and 1.8 instructions a clock; the main loop alone, without
+// the producers' work, runs at 91 % of that pipe's rate.  A share of the exponentials as polynomials on the
+// fp32 pipe was slower (one pair in 4: +5 %): the instructions it adds cost more than the
+// pipe it frees.
 //
 // A call with few channels would leave the GPU empty and walk a long chain, so
 // the time axis is split over the R CTAs of a cluster: each CTA first runs its
@@ -69,7 +78,6 @@ __device__ __forceinline__ float2 softplus2(float2 v) {
   q = fma2(q, e, both(0.9999999403953552f));
   return unpack2(fma2(q, e, pack2(fmaxf(v.x, 0.f), fmaxf(v.y, 0.f))));
 }
-__device__ __forceinline__ float softplus_f(float v) { return softplus2(make_float2(v, 0.f)).x; }
 __device__ __forceinline__ float gate_f(float z) { return z * rcp_approx(1.f + exp2_approx(-z * kLog2e)); }
 
 __device__ __forceinline__ int length_of(const gam_scan_args& p, int b) {
@@ -360,11 +368,12 @@ scan_kernel(const gam_scan_args p, const int sms, const bool pair) {
     };
     if (SPLIT && threadIdx.x >= kLanes) {
       // while the lanes run tile k: the y of the one before goes out, the one after is made ready
-      auto pass = [&](auto out_tag) {
+      auto pass = [&](auto out_tag, bool joined) {
         constexpr bool OUT = decltype(out_tag)::value;
         fetch(out_tag, 0);
         fetch(out_tag, 1);
         asm volatile("cp.async.wait_group 1;" ::: "memory");
+        if (joined) __syncthreads();                 // the lanes have read the pieces' end states, whose place the tiles take
         if (tiles > 0) prepare(out_tag, 0);
         __syncthreads();
         for (int k = 0; k < tiles; ++k) {
@@ -377,12 +386,12 @@ scan_kernel(const gam_scan_args p, const int sms, const bool pair) {
         if (OUT && tiles > 0) finish(tiles - 1);
         asm volatile("cp.async.wait_group 0;" ::: "memory");
       };
-      if (R == 1 || rank == 0) pass(std::true_type());
-      else if (rank < R - 1) pass(std::false_type());
+      if (R == 1 || rank == 0) pass(std::true_type(), false);
+      else if (rank < R - 1) pass(std::false_type(), false);
       if (R > 1) {
         cluster.sync();
         cluster.sync();
-        if (rank > 0) pass(std::true_type());
+        if (rank > 0) pass(std::true_type(), true);
       }
       zeros();
       return;
@@ -540,6 +549,7 @@ scan_kernel(const gam_scan_args p, const int sms, const bool pair) {
           }
         }
       }
+      __syncthreads();                               // the producers may put the first tile there now
       pass(std::true_type());
     }
   } else {
@@ -767,6 +777,7 @@ extern "C" gam_status gam_selective_scan(const gam_scan_args* args, void* stream
     if (!is_float_dtype(p.dtype)) return op_fail(GAM_ERR_INVALID_ARG, "dtype must be f32, f16 or bf16");
     if (p.batch < 0 || p.t_max < 0 || p.d < 1) return op_fail(GAM_ERR_INVALID_ARG, "batch >= 0, t_max >= 0 and d >= 1");
     if (p.n < 1 || p.n > 64) return op_fail(GAM_ERR_SHAPE, "n must be 1 .. 64");
+    if (p.t_max > kMaxDim || p.d > kMaxDim) return op_fail(GAM_ERR_CAPACITY, "t_max and d up to 2^30");
     if (p.batch == 0) return GAM_OK;
     if (!p.a || (p.t_max > 0 && (!p.x || !p.dt || !p.b || !p.c || !p.y)))
       return op_fail(GAM_ERR_INVALID_ARG, "null pointer");

@@ -5,7 +5,10 @@
 // A thread owns V channels (one 16-byte access; one channel when the rows are
 // not 16-byte aligned) and a segment of the time axis.  It keeps the last
 // taps - 1 rows in registers, so inside a segment every input is read once, and
-// has R rows on their way at a time (the bound is memory).
+// has R rows on their way while it works on R others (the bound is memory).  The
+// multiply-adds go two channels at a time in packed fp32.  32 clips of up to 749
+// frames of 2048 channels in fp16 (150 MB): 34 us, 4.4 TB/s; with 128 registers
+// instead of 168, for more threads to an SM, 64 us (spills).
 #include <algorithm>
 
 #include "stream_ops.cuh"
@@ -155,7 +158,8 @@ gam_status launch(int taps, ConvArgs p, int sms, cudaStream_t s) {
   const int64_t columns = (int64_t)p.vecs * p.batch, want = (int64_t)sms * 512;
   const int64_t segs = std::max<int64_t>(1, (want + columns - 1) / columns);
   const int R = p.t_max == 1 ? 1 : p.t_max / segs >= 8 ? 8 : 2;
-  p.seg = std::max(R, (int)((p.t_max + segs - 1) / segs + R - 1) / R * R);
+  // A segment is no shorter than the history, so that only segment 0 reads the state that it may replace.
+  p.seg = (int)((std::max<int64_t>((p.t_max + segs - 1) / segs, taps - 1) + R - 1) / R * R);
   p.segs = p.t_max ? (p.t_max + p.seg - 1) / p.seg : 1;
   const int64_t grid = (columns * p.segs + kThreads - 1) / kThreads;
   if (grid > INT32_MAX) return op_fail(GAM_ERR_CAPACITY, "batch * t_max * d too large for one call");
@@ -180,6 +184,7 @@ extern "C" gam_status gam_short_conv(const void* x, int dtype, int64_t x_batch_s
     if (act != GAM_ACT_NONE && act != GAM_ACT_SWISH) return op_fail(GAM_ERR_INVALID_ARG, "act must be none or swish");
     if (batch < 0 || t_max < 0 || d < 1) return op_fail(GAM_ERR_INVALID_ARG, "batch >= 0, t_max >= 0 and d >= 1");
     if (taps < 2 || taps > 8) return op_fail(GAM_ERR_SHAPE, "taps must be 2 .. 8");
+    if (t_max > kMaxDim || d > kMaxDim) return op_fail(GAM_ERR_CAPACITY, "t_max and d up to 2^30");
     if (batch == 0) return GAM_OK;
     if (!w || (t_max > 0 && (!x || !y))) return op_fail(GAM_ERR_INVALID_ARG, "null pointer");
     const int es = dtype_size(dtype);

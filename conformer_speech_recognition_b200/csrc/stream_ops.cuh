@@ -142,21 +142,13 @@ __device__ __forceinline__ float sigmoid_f(float v) {
 }
 __device__ __forceinline__ float swish_f(float v) { return v * sigmoid_f(v); }
 
-__device__ __forceinline__ float activate(float v, int act) {
-  switch (act) {
-    case GAM_ACT_SWISH: return swish_f(v);
-    case GAM_ACT_SIGMOID: return sigmoid_f(v);
-    case GAM_ACT_TANH: return tanhf(v);
-    default: return v;
-  }
-}
-
 // --- host side -----------------------------------------------------------------
 
 inline gam_status op_fail(gam_status s, const std::string& msg) {
   set_context_free_error(msg);
   return s;
 }
+constexpr int kMaxDim = 1 << 30;  // of one dimension: sums of two stay in 32 bits
 inline bool is_float_dtype(int t) { return t == GAM_DTYPE_F32 || t == GAM_DTYPE_F16 || t == GAM_DTYPE_BF16; }
 inline int dtype_size(int t) { return t == GAM_DTYPE_F32 ? 4 : 2; }
 inline bool aligned(const void* p, size_t bytes) { return reinterpret_cast<uintptr_t>(p) % bytes == 0; }

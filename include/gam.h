@@ -359,8 +359,9 @@ gam_status gam_stream_push(gam_stream* st, const float* samples_host, int64_t n,
  * statistics and scan states are fp32 and an output is rounded once.  Strides
  * are in elements; the last dimension is contiguous.  Pointers need the
  * alignment of their element type only (16-byte aligned rows are faster),
- * except packed weights, which need 16 bytes.  Outputs must not overlap inputs
- * or one another unless a call says so.  A call with no rows or no sequences
+ * except packed weights, which need 16 bytes.  A dimension is at most 2^30
+ * (GAM_ERR_CAPACITY).  Outputs must not overlap inputs or one another unless a
+ * call says so.  A call with no rows or no sequences
  * does nothing and succeeds. */
 
 /* Activation of an operator's result or gate: v, v sigmoid(v), sigmoid(v) or

@@ -172,7 +172,8 @@ def conv_check(y, new, xf, w, b, lens, sf, act, dtype, exact_state):
     (1, 130, 8, 3, "none", True, False, None), (5, 37, 40, 4, "swish", True, True, [37, 0, 1, 2, 36]),
     (4, 100, 33, 5, "none", False, True, [100, 17, 16, 3]), (2, 65, 1032, 6, "swish", True, False, [65, -3]),
     (2, 29, 24, 7, "swish", False, True, [1000, 5]), (64, 1, 256, 4, "swish", True, True, [i % 2 for i in range(64)]),
-    (1, 3001, 24, 4, "none", True, True, [2999])])
+    (1, 3001, 24, 4, "none", True, True, [2999]), (3, 9, 40, 8, "none", True, True, [9, 3, 8]),
+    (40, 50, 2048, 4, "swish", True, True, [(i * 7) % 51 for i in range(40)])])
 def test_conv(dtype, B, T, d, taps, act, bias, state, lens):
     rng = np.random.default_rng(B * 100 + T + d + taps)
     x, xf = normal(rng, B, T, d, dtype=dtype)
@@ -261,7 +262,8 @@ def scan_call(t, lengths=None, **more):
     (1, 2, 40, 8, True, False, None), (2, 17, 65, 3, True, True, [17, 9]), (5, 40, 24, 16, True, True, [40, 0, 1, 39, 16]),
     (2, 33, 130, 12, False, False, [33, 32]), (1, 300, 48, 32, True, True, None), (2, 70, 17, 64, True, True, [70, 1000]),
     (2, 130, 96, 33, False, True, [-5, 129]), (1, 1500, 16, 16, True, True, [1499]), (64, 3, 64, 16, True, True, None),
-    (1, 700, 200, 20, True, False, None)])
+    (1, 700, 200, 20, True, False, None), (1, 900, 37, 9, True, True, [801]), (2, 640, 8, 64, False, True, [640, 3]),
+    (1, 520, 24, 5, True, True, None), (40, 9, 1024, 16, True, True, [i % 10 for i in range(40)])])
 def test_scan(dtype, B, T, d, n, z, state, lens):
     torch = _torch()
     t, f = scan_inputs(B * 31 + T + d + n, B, T, d, n, dtype, z, state)

@@ -62,7 +62,7 @@ LINEAR = dict(x=P, dtype=1, ldx=128, packed=P, scale=P, bias=None, act=0, rows=2
     (dict(packed=None), "GAM_ERR_INVALID_ARG"), (dict(scale=None), "GAM_ERR_INVALID_ARG"),
     (dict(y=None), "GAM_ERR_INVALID_ARG"), (dict(packed=P + 8), "GAM_ERR_INVALID_ARG"), (dict(x=P + 1), "GAM_ERR_INVALID_ARG"),
     (dict(bias=P + 2), "GAM_ERR_INVALID_ARG"), (dict(ldx=127), "GAM_ERR_SHAPE"), (dict(ldy=31), "GAM_ERR_SHAPE"),
-    (dict(y=P), "GAM_ERR_INVALID_ARG")])
+    (dict(y=P), "GAM_ERR_INVALID_ARG"), (dict(n=2 ** 30 + 1, ldy=2 ** 31), "GAM_ERR_CAPACITY")])
 def test_linear_refusals(L, change, name):
     a = dict(LINEAR, **change)
     _refused(L.gam_quant_linear(*a.values(), None), name)
@@ -82,7 +82,8 @@ CONV = dict(x=P, dtype=1, xb=320, xr=32, w=P, bias=None, taps=4, act=1, batch=2,
     (dict(d=0), "GAM_ERR_INVALID_ARG"), (dict(x=None), "GAM_ERR_INVALID_ARG"), (dict(w=None), "GAM_ERR_INVALID_ARG"),
     (dict(y=None), "GAM_ERR_INVALID_ARG"), (dict(y=P), "GAM_ERR_INVALID_ARG"), (dict(x=P + 1), "GAM_ERR_INVALID_ARG"),
     (dict(si=P + 1), "GAM_ERR_INVALID_ARG"), (dict(lengths=P + 2), "GAM_ERR_INVALID_ARG"),
-    (dict(yr=31), "GAM_ERR_SHAPE"), (dict(yb=319), "GAM_ERR_SHAPE")])
+    (dict(yr=31), "GAM_ERR_SHAPE"), (dict(yb=319), "GAM_ERR_SHAPE"),
+    (dict(t=2 ** 30 + 1), "GAM_ERR_CAPACITY"), (dict(d=2 ** 30 + 1), "GAM_ERR_CAPACITY")])
 def test_conv_refusals(L, change, name):
     a = dict(CONV, **change)
     _refused(L.gam_short_conv(*a.values(), None), name)
@@ -107,7 +108,8 @@ def _scan(L, **change):
     (dict(x=0), "GAM_ERR_INVALID_ARG"), (dict(dt=0), "GAM_ERR_INVALID_ARG"), (dict(a=0), "GAM_ERR_INVALID_ARG"),
     (dict(b=0), "GAM_ERR_INVALID_ARG"), (dict(c=0), "GAM_ERR_INVALID_ARG"), (dict(y=0), "GAM_ERR_INVALID_ARG"),
     (dict(y=P), "GAM_ERR_INVALID_ARG"), (dict(b=P + 1), "GAM_ERR_INVALID_ARG"), (dict(a=P + 2), "GAM_ERR_INVALID_ARG"),
-    (dict(state_in=P + 2), "GAM_ERR_INVALID_ARG"), (dict(yr=31), "GAM_ERR_SHAPE"), (dict(yb=319), "GAM_ERR_SHAPE")])
+    (dict(state_in=P + 2), "GAM_ERR_INVALID_ARG"), (dict(yr=31), "GAM_ERR_SHAPE"), (dict(yb=319), "GAM_ERR_SHAPE"),
+    (dict(t=2 ** 30 + 1), "GAM_ERR_CAPACITY"), (dict(d=2 ** 30 + 1), "GAM_ERR_CAPACITY")])
 def test_scan_refusals(L, change, name):
     _refused(_scan(L, **change), name)
 
