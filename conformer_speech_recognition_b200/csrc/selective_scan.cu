@@ -61,6 +61,41 @@ __device__ __forceinline__ float rcp_approx(float v) {
   return r;
 }
 
+// 2^x for two values on the fp32 and integer pipes: x = n + f, n whole and |f| <= 1/2 by
+// the rounding of an addition, 2^f by the polynomial of degree 5 with 2^0 = 1 and the
+// least largest relative error (8e-8; 1.6e-7 evaluated in fp32, 6e-8 for |f| < 0.001), 2^n
+// into the exponent.  Below -125 the result stays 2^-125, which is as good as 0 beside any
+// input; 128 gives infinity; NaN stays.
+__device__ __forceinline__ float clamp_exponent(float v) {
+  float r;
+  asm("{\n\t.reg .f32 t;\n\tmax.NaN.f32 t, %1, 0fC2FA0000;\n\tmin.NaN.f32 %0, t, 0f43000000;\n\t}" : "=f"(r) : "f"(v));
+  return r;
+}
+__device__ __forceinline__ u64 exp2_poly2(u64 x) {
+  const float2 c = unpack2(x);
+  const u64 v = pack2(clamp_exponent(c.x), clamp_exponent(c.y));
+  const u64 one = both(1.f);
+  const u64 t = fma2(v, one, both(12582912.f));      // 1.5 * 2^23: its last bit counts ones
+  const u64 f = fma2(fma2(t, one, both(-12582912.f)), both(-1.f), v);
+  u64 q = both(0.0013274633092805743f);
+  q = fma2(q, f, both(0.009671961888670921f));
+  q = fma2(q, f, both(0.055506784468889236f));
+  q = fma2(q, f, both(0.24022234976291656f));
+  q = fma2(q, f, both(0.6931470632553101f));
+  q = fma2(q, f, one);
+  const float2 n = unpack2(t), r = unpack2(q);
+  return pack2(__int_as_float(__float_as_int(r.x) + (__float_as_int(n.x) << 23)),
+               __int_as_float(__float_as_int(r.y) + (__float_as_int(n.y) << 23)));
+}
+// A decay 2^x.  A state that decays slowly adds up the decays' errors over many frames: with the hardware's 2^x
+// (2^-22) an fp32 call's outputs came out 1e-6 off, so fp32 calls take the polynomial; beside the rounding of a
+// 16-bit output the hardware's is as good.
+template <typename T>
+__device__ __forceinline__ u64 decay2(u64 x) {
+  if constexpr (sizeof(T) == 4) return exp2_poly2(x);
+  else return exp2_approx2(x);
+}
+
 // log(1 + e^v) = max(v, 0) + log1p(e), e = e^-|v| in (0, 1], for two values.  log1p(e) / e
 // by the polynomial of degree 8 with the least largest relative error on [0, 1] (3e-8;
 // 1.7e-7 evaluated in fp32): nothing cancels, so small steps keep their digits.
@@ -443,7 +478,7 @@ scan_kernel(const gam_scan_args p, const int sms, const bool pair) {
 #pragma unroll
               for (int j = 0; j < CH; ++j) {
                 u64& hh = h[j][2 * i + q];
-                const u64 decay = exp2_approx2(mul2(s2[j], a[j][2 * i + q]));
+                const u64 decay = decay2<T>(mul2(s2[j], a[j][2 * i + q]));
                 hh = fma2(decay, hh, mul2(sx2[j], q ? bv.y : bv.x));
                 if (OUT) y2[j] = i + q ? fma2(q ? cv.y : cv.x, hh, y2[j]) : mul2(cv.x, hh);
               }
@@ -542,7 +577,7 @@ scan_kernel(const gam_scan_args p, const int sms, const bool pair) {
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
               u64& hh = h[j][2 * i + k];
-              const u64 decay = exp2_approx2(mul2(both(q), a[j][2 * i + k]));
+              const u64 decay = decay2<T>(mul2(both(q), a[j][2 * i + k]));
               // the first piece's end state is whole already
               hh = r ? fma2(decay, hh, k ? end.y : end.x) : (k ? end.y : end.x);
             }
@@ -654,9 +689,12 @@ __global__ void __launch_bounds__(256) step_kernel(const gam_scan_args p) {
       const float st = j ? s.y : s.x, xv = from_bits<T>(ux[j]), sx = st * xv, e = st * kLog2e;
       float v = 0.f;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        h[j][i] = fmaf(exp2_approx(e * a[j][i]), h[j][i], sx * bv[i]);
+      for (int i = 0; i < 4; i += 2) {
+        const float2 decay = unpack2(decay2<T>(pack2(e * a[j][i], e * a[j][i + 1])));
+        h[j][i] = fmaf(decay.x, h[j][i], sx * bv[i]);
+        h[j][i + 1] = fmaf(decay.y, h[j][i + 1], sx * bv[i + 1]);
         v = fmaf(cv[i], h[j][i], v);
+        v = fmaf(cv[i + 1], h[j][i + 1], v);
       }
 #pragma unroll
       for (int o = L / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
