@@ -18,7 +18,7 @@
 // thread does both, with two channels to a lane (32 x 390 frames of 2048 channels: 179 us,
 // with producers 249), which halves the reads of b and c.
 //
-// What it measured (16 states): 12.5 k frames of 2048 channels in 207 us, the special-function
+// What it measured (16 states): 12.5 k frames of 2048 channels in 209 us, the special-function
 // pipe 57 % busy (exponentials and the gates' reciprocals) and 1.8 instructions a clock; the main loop alone, without
 // the producers' work, runs at 91 % of that pipe's rate.  A share of the exponentials as polynomials on the
 // fp32 pipe was slower (one pair in 4: +5 %): the instructions it adds cost more than the
@@ -87,13 +87,17 @@ __device__ __forceinline__ u64 exp2_poly2(u64 x) {
   return pack2(__int_as_float(__float_as_int(r.x) + (__float_as_int(n.x) << 23)),
                __int_as_float(__float_as_int(r.y) + (__float_as_int(n.y) << 23)));
 }
-// A decay 2^x.  A state that decays slowly adds up the decays' errors over many frames: with the hardware's 2^x
-// (2^-22) an fp32 call's outputs came out 1e-6 off, so fp32 calls take the polynomial; beside the rounding of a
-// 16-bit output the hardware's is as good.
+// A decay 2^(s a).  A state that decays slowly adds up the decays' errors over many frames: with the hardware's
+// 2^x (2^-22) an fp32 call's outputs came out 1e-6 off, so fp32 calls take the polynomial.  16-bit calls keep the
+// hardware's, but not its mean error: that is -6e-9 for x in -0.003 .. 0 and -2e-8 in -0.7 .. -0.003 (measured),
+// so x is raised by kRaise, which the multiply-add gives for nothing and which leaves 7e-9 either way (49
+// sequences of 88 frames, fp16: states 1.6e-6 off without it, 7.6e-7 with).  2^kRaise is 1 in 32 bits: a step of 0
+// leaves the state as it was.
+constexpr float kRaise = 1.9e-8f;
 template <typename T>
-__device__ __forceinline__ u64 decay2(u64 x) {
-  if constexpr (sizeof(T) == 4) return exp2_poly2(x);
-  else return exp2_approx2(x);
+__device__ __forceinline__ u64 decay2(u64 s, u64 a) {
+  if constexpr (sizeof(T) == 4) return exp2_poly2(mul2(s, a));
+  else return exp2_approx2(fma2(s, a, both(kRaise)));
 }
 
 // log(1 + e^v) = max(v, 0) + log1p(e), e = e^-|v| in (0, 1], for two values.  log1p(e) / e
@@ -478,7 +482,7 @@ scan_kernel(const gam_scan_args p, const int sms, const bool pair) {
 #pragma unroll
               for (int j = 0; j < CH; ++j) {
                 u64& hh = h[j][2 * i + q];
-                const u64 decay = decay2<T>(mul2(s2[j], a[j][2 * i + q]));
+                const u64 decay = decay2<T>(s2[j], a[j][2 * i + q]);
                 hh = fma2(decay, hh, mul2(sx2[j], q ? bv.y : bv.x));
                 if (OUT) y2[j] = i + q ? fma2(q ? cv.y : cv.x, hh, y2[j]) : mul2(cv.x, hh);
               }
@@ -577,7 +581,7 @@ scan_kernel(const gam_scan_args p, const int sms, const bool pair) {
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
               u64& hh = h[j][2 * i + k];
-              const u64 decay = decay2<T>(mul2(both(q), a[j][2 * i + k]));
+              const u64 decay = decay2<T>(both(q), a[j][2 * i + k]);
               // the first piece's end state is whole already
               hh = r ? fma2(decay, hh, k ? end.y : end.x) : (k ? end.y : end.x);
             }
@@ -690,7 +694,7 @@ __global__ void __launch_bounds__(256) step_kernel(const gam_scan_args p) {
       float v = 0.f;
 #pragma unroll
       for (int i = 0; i < 4; i += 2) {
-        const float2 decay = unpack2(decay2<T>(pack2(e * a[j][i], e * a[j][i + 1])));
+        const float2 decay = unpack2(decay2<T>(both(e), pack2(a[j][i], a[j][i + 1])));
         h[j][i] = fmaf(decay.x, h[j][i], sx * bv[i]);
         h[j][i + 1] = fmaf(decay.y, h[j][i + 1], sx * bv[i + 1]);
         v = fmaf(cv[i], h[j][i], v);
