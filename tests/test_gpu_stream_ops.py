@@ -319,6 +319,18 @@ def test_scan_strides_and_pieces(dtype):
     scan_check(torch.cat(parts, 1), state, f, [T] * B, dtype)
 
 
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("B,T,d,n", [(3, 1, 33, 5), (2, 60, 40, 16), (1, 1500, 16, 16), (40, 9, 1024, 16)])
+def test_scan_steps_of_zero_keep_the_state(dtype, B, T, d, n):
+    """A decay of 2^0 is 1 and an input of weight 0 is 0: such channels end with the state they began with, bit for bit."""
+    torch = _torch()
+    t, _ = scan_inputs(12 + T, B, T, d, n, dtype)
+    t["dt"], t["dt_bias"] = t["dt"].abs(), None
+    t["dt"][..., ::3] = 0
+    _, new = scan_call(t, dt_softplus=False)
+    assert torch.equal(new[:, ::3], t["state"][:, ::3]) and not torch.equal(new, t["state"])
+
+
 def test_scan_no_frames_hands_the_state_on():
     torch = _torch()
     t, _ = scan_inputs(10, 2, 1, 24, 7, "f32")
