@@ -10,9 +10,9 @@
 // and tensor memory that tcgen05 works on).  The integers are exact in both 16-bit
 // types, so a group's sum is that of q x itself and is scaled in fp32 by the group's scale.
 //
-// What it measured: one row of 768 x 768 in 2.4 us (launch and one trip to memory), 16 rows of
-// 16384 x 4096 in bf16 in 19.5 us (36 MB of weights, 1.9 TB/s): 8.0 M instructions at 1.7 a clock,
-// 16 warps to an SM by their registers; the tensor pipe is 23 % busy.
+// What it measured: one row of 768 x 768 in 2.4 us (launch and one trip to memory); one row of
+// 16384 x 4096 in 14 us (36 MB of weights, 2.6 TB/s) and 16 rows in 19.5 us: 8.0 M instructions at
+// 1.7 a clock, 16 warps to an SM by their registers, lines in the L1 77 % of the time.
 //
 // The words' nibble order gives adjacent pairs by one shift and mask, and a lane's 16
 // weights of a group are 16 consecutive k, so its fragments of x are 16 consecutive
@@ -145,7 +145,8 @@ struct LinearArgs {
   int64_t ldx, ldy;
   int act, rows, n, groups;   // groups = k / 64
   int wide;                   // x rows are 16-byte aligned
-  int kw, per, chunk;         // staged form: warps that share a tile's K, groups of a stage, groups of x held at a time
+  int kw, per;                // staged form: warps that share a tile's K, groups of a stage
+  int chunk;                  // shared and staged forms: groups of x held at a time
 };
 
 // ---- few rows or few weights ----
@@ -341,17 +342,20 @@ gam_status launch_thin(const LinearArgs& p, int sms, cudaStream_t s) {
   return launch_status(cudaLaunchKernelEx(&cfg, quant_linear_thin_kernel<T, MT, NT>, p));
 }
 
-// ---- many weights, fp32 ----
-// Splitting x into its parts takes more instructions than a tile's MMAs, so with many tiles it is done once per
-// CTA: the parts lie in shared memory (in chunks of K, rows 16 bytes apart beyond their length, for the banks)
-// and 16 warps read their fragments there.  Weights reach a warp through its own ring of cp.async stages (16 rows
-// x 128 bytes, 4 groups): fully coalesced, no barrier between warps.  Inside a stage the 32-byte slot of group G
-// of row r is G ^ (r & 3), which makes the 8-byte fragment reads free of bank conflicts.  K is split over KW warps
-// (1 .. 16, a power of two) such that the tiles times KW about fill the GPU's SMs with 16 warps each.
-constexpr int kWarps = 16, kStages = 3, kStageBytes = 2048;
-constexpr int kRingBytes = kWarps * kStages * kStageBytes;
+// ---- many weights, up to 8 rows, 16-bit ----
+// A warp's loads of 8 rows touch 8 lines each, and that, not the bytes, was what the form above took its time
+// for with many weights: the L1 moved lines 69 % of the time, for scales, weights and x.  Here loads from memory
+// take whole 128-byte lines: a CTA of 8 warps takes 256 outputs, a warp 32 of them; weights reach it 4 groups
+// (a run: 32 rows x 128 bytes) at a time by cp.async, the next run while it works on one, one scale load serves
+// a run (lane t holds group t's, and hands it on by a shuffle), and x lies in shared memory for all warps.
+// K is split over a cluster, whose CTAs exchange their sums.  1 x 16384 x 4096: 21 us above, 14 here
+// (2.6 TB/s); three runs under way leave less room for x and took 16.5.
+//
+// The 32-byte slot of group G of row r is G ^ (r & 3) in a run, and rows of x lie 16 bytes beyond their length:
+// fragment reads are free of bank conflicts.
 constexpr int kMaxSmem = 227 * 1024;
-constexpr int kXBytes = kMaxSmem - kRingBytes;   // for x
+constexpr int kSharedWarps = 8, kRunBytes = 32 * 128, kRuns = 2;
+constexpr int kSharedSmem = 112 * 1024;  // two CTAs to an SM
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
@@ -369,6 +373,207 @@ __device__ __forceinline__ uint4 lds16(uint32_t at) {
   asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at) : "memory");
   return v;
 }
+
+template <typename T>
+__global__ void __launch_bounds__(kSharedWarps * 32, 2) quant_linear_shared_kernel(const LinearArgs p) {
+  constexpr int NT = 2, kThreads = kSharedWarps * 32;
+  extern __shared__ __align__(128) uint8_t smem[];
+  cg::cluster_group cluster = cg::this_cluster();
+  const int R = cluster.num_blocks(), rank = cluster.block_rank();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const int o0 = (blockIdx.x / R * kSharedWarps + warp) * NT * 16;
+  const bool live = o0 < p.n;
+  const int runs = (p.groups + 3) / 4;
+  const int k_lo = (int)((int64_t)runs * rank / R) * 4, k_hi = min((int)((int64_t)runs * (rank + 1) / R) * 4, p.groups);
+  const int64_t row_bytes = (int64_t)p.groups * 32;
+  uint8_t* const xs = smem + kSharedWarps * kRuns * kRunBytes;
+  const uint32_t ring = (uint32_t)__cvta_generic_to_shared(smem) + warp * kRuns * kRunBytes;
+  // a lane copies 16 bytes of rows 4 j + lane / 8
+  const int cr = lane >> 3, cc = lane & 7;
+  const uint32_t copy_to = ring + cr * 128 + ((((cc >> 1) ^ cr) << 1) | (cc & 1)) * 16;
+  const uint32_t frag = ring + g * 128 + t * 8;
+  // rows of x behind the last: row 0, dropped below
+  const int xrow = p.chunk * 128 + 16;
+  const uint32_t xf = (uint32_t)__cvta_generic_to_shared(xs) + (g < p.rows ? g : 0) * xrow + t * 32;
+  const __half* sc[NT][2];
+#pragma unroll
+  for (int i = 0; i < NT; ++i)
+#pragma unroll
+    for (int h = 0; h < 2; ++h) sc[i][h] = p.scale + (int64_t)min(o0 + i * 16 + h * 8 + g, p.n - 1) * p.groups + t;
+  // rows past n are not copied: what lies there reaches only outputs that are dropped
+  const uint8_t* src = p.packed + (o0 + cr) * row_bytes + (int64_t)k_lo * 32 + cc * 16;
+  const UnpackConst<T> consts;
+
+  uint32_t scales[kRuns - 1][NT][2] = {};                // of the runs on their way
+  auto issue = [&](int k, int slot, uint32_t (&to)[NT][2]) {  // the run of group k
+    if (live && k < k_hi) {
+      const int ng = min(4, k_hi - k);
+      const uint8_t* from = src;
+      if ((cc >> 1) < ng) {
+        if (o0 + NT * 16 <= p.n) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j, from += 4 * row_bytes) cp_async16(copy_to + slot * kRunBytes + j * 512, from);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 8; ++j, from += 4 * row_bytes)
+            if (o0 + j * 4 + cr < p.n) cp_async16(copy_to + slot * kRunBytes + j * 512, from);
+        }
+      }
+      src += 128;
+      if (t < ng)
+#pragma unroll
+        for (int i = 0; i < NT; ++i)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) to[i][h] = *reinterpret_cast<const unsigned short*>(sc[i][h] + k);
+    }
+    cp_commit();
+  };
+  u64 acc[NT][2] = {};                                   // pairs: outputs g (and g + 8) of rows 2 t and 2 t + 1
+  auto group = [&](int G, uint32_t at_w, uint32_t at_x, const uint32_t (&s)[NT][2]) {
+    const uint4 xv[2] = {lds16(xf + at_x), lds16(xf + at_x + 16)};
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+      const uint2 wa = lds8(at_w + i * 2048), wb = lds8(at_w + i * 2048 + 1024);
+      float c[4];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        uint32_t pa[4], pb[4];
+        unpack8(h ? wa.y : wa.x, pa, consts);
+        unpack8(h ? wb.y : wb.x, pb, consts);
+        const uint32_t a0[4] = {pa[0], pb[0], pa[1], pb[1]}, a1[4] = {pa[2], pb[2], pa[3], pb[3]};
+        if (h == 0) mma16816<true>(c, a0, xv[h].x, xv[h].y, T());
+        else mma16816<false>(c, a0, xv[h].x, xv[h].y, T());
+        mma16816<false>(c, a1, xv[h].z, xv[h].w, T());
+      }
+      const uint32_t sa = __shfl_sync(0xffffffffu, s[i][0], (lane & 28) | G), sb = __shfl_sync(0xffffffffu, s[i][1], (lane & 28) | G);
+      const float fa = __half2float(__ushort_as_half((unsigned short)sa)), fb = __half2float(__ushort_as_half((unsigned short)sb));
+      acc[i][0] = fma2(both(fa), pack2(c[0], c[1]), acc[i][0]);
+      acc[i][1] = fma2(both(fb), pack2(c[2], c[3]), acc[i][1]);
+    }
+  };
+
+#pragma unroll
+  for (int u = 0; u < kRuns - 1; ++u) issue(k_lo + 4 * u, u, scales[u]);
+  int slot = 0;
+  for (int c0 = k_lo; c0 < k_hi; c0 += p.chunk) {
+    const int held = min(p.chunk, k_hi - c0), pieces = held * 8;
+    if (c0 > k_lo) __syncthreads();                      // the chunk before is read
+    const int per_row = p.rows == 1 ? kThreads : 32;      // threads of a row
+    for (int r = threadIdx.x / per_row; r < p.rows; r += kThreads / per_row) {
+      const T* from = (const T*)p.x + r * p.ldx + (int64_t)c0 * 64;
+      uint8_t* to = xs + r * xrow;
+      for (int c = threadIdx.x % per_row; c < pieces; c += per_row) {
+        if (p.wide) {
+          cp_async16((uint32_t)__cvta_generic_to_shared(to + c * 16), from + c * 8);
+        } else {
+          Vec<T, 8> v;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) v.v[i] = from[c * 8 + i];
+          *reinterpret_cast<Vec<T, 8>*>(to + c * 16) = v;
+        }
+      }
+    }
+    cp_commit();
+    cp_wait<0>();
+    __syncthreads();
+    for (int k = c0; k < c0 + held; k += 4) {
+      uint32_t s[NT][2];
+#pragma unroll
+      for (int i = 0; i < NT; ++i)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          s[i][h] = scales[0][i][h];
+#pragma unroll
+          for (int u = 0; u + 2 < kRuns; ++u) scales[u][i][h] = scales[u + 1][i][h];
+        }
+      // the new run's slot was read before the last __syncwarp
+      issue(k + 4 * (kRuns - 1), slot == 0 ? kRuns - 1 : slot - 1, scales[kRuns - 2]);
+      cp_wait<kRuns - 1>();
+      __syncwarp();                                      // every lane's copies of this run are in
+      const int ng = live ? min(4, k_hi - k) : 0;
+      const uint32_t at = frag + slot * kRunBytes, at_x = (k - c0) * 128;
+      if (ng == 4) {
+#pragma unroll
+        for (int G = 0; G < 4; ++G) group(G, at + (G ^ (g & 3)) * 32, at_x + G * 128, s);
+      } else {
+#pragma unroll 1
+        for (int G = 0; G < ng; ++G) group(G, at + (G ^ (g & 3)) * 32, at_x + G * 128, s);
+      }
+      __syncwarp();
+      slot = slot + 1 == kRuns ? 0 : slot + 1;
+    }
+  }
+  cp_wait<0>();
+  if (R > 1) {
+    // warp w's sums are added up by CTA w % R of the cluster: [w / R][rank][sum][lane] over the idle ring
+    u64* const join = reinterpret_cast<u64*>(smem);
+    constexpr int SUMS = NT * 2;
+    cluster.sync();
+    u64* to = cluster.map_shared_rank(join, warp % R) + ((warp / R) * R + rank) * SUMS * 32 + lane;
+#pragma unroll
+    for (int i = 0; i < SUMS; ++i) to[i * 32] = (&acc[0][0])[i];
+    cluster.sync();
+    if (warp % R != rank) return;
+#pragma unroll
+    for (int i = 0; i < SUMS; ++i) {
+      u64 v = 0;
+      for (int q = 0; q < R; ++q) v = fma2(both(1.f), join[((warp / R) * R + q) * SUMS * 32 + i * 32 + lane], v);
+      (&acc[0][0])[i] = v;
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < NT; ++i)
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int o = o0 + i * 16 + h * 8 + g;
+      if (o >= p.n) continue;
+      const float bias = p.bias ? p.bias[o] : 0.f;
+      const float2 sums = unpack2(acc[i][h]);
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int r = 2 * t + e;
+        const float v = (e ? sums.y : sums.x) * kUnpackScale<T> + bias;
+        if (r < p.rows) ((T*)p.y)[r * p.ldy + o] = from_f<T>(p.act == GAM_ACT_SWISH ? swish_f(v) : v);
+      }
+    }
+}
+
+template <typename T>
+gam_status launch_shared(LinearArgs p, int sms, cudaStream_t s) {
+  // K over a cluster of R CTAs while two CTAs to an SM hold them all at once and each has two runs
+  const int ctas = (p.n + kSharedWarps * 32 - 1) / (kSharedWarps * 32);
+  int R = 1;
+  while (R < 8 && ctas * R <= sms && p.groups >= R * 2 * 4) R *= 2;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(ctas * R);
+  cfg.blockDim = dim3(kSharedWarps * 32);
+  // of x: a CTA's share of K, or as many whole runs of it as fit
+  constexpr int ring = kSharedWarps * kRuns * kRunBytes;
+  p.chunk = std::min(((p.groups + 3) / 4 + R - 1) / R, ((kSharedSmem - ring) / p.rows - 16) / 512) * 4;
+  cfg.dynamicSmemBytes = ring + p.rows * (p.chunk * 128 + 16);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = R;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = R > 1 ? 1 : 0;
+  auto kernel = quant_linear_shared_kernel<T>;
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)cfg.dynamicSmemBytes);
+  if (e != cudaSuccess) return launch_status(e);
+  return launch_status(cudaLaunchKernelEx(&cfg, kernel, p));
+}
+
+// ---- many weights, fp32 ----
+// Splitting x into its parts takes more instructions than a tile's MMAs, so with many tiles it is done once per
+// CTA: the parts lie in shared memory (in chunks of K, rows 16 bytes apart beyond their length, for the banks)
+// and 16 warps read their fragments there.  Weights reach a warp through its own ring of cp.async stages (16 rows
+// x 128 bytes, 4 groups): fully coalesced, no barrier between warps.  Inside a stage the 32-byte slot of group G
+// of row r is G ^ (r & 3), which makes the 8-byte fragment reads free of bank conflicts.  K is split over KW warps
+// (1 .. 16, a power of two) such that the tiles times KW about fill the GPU's SMs with 16 warps each.
+constexpr int kWarps = 16, kStages = 3, kStageBytes = 2048;
+constexpr int kRingBytes = kWarps * kStages * kStageBytes;
+constexpr int kXBytes = kMaxSmem - kRingBytes;   // for x
 
 // ke elements from k0 on of x's rows to shared memory in three bf16 parts.  The warps share the rows evenly.
 __device__ __forceinline__ void stage_x(const LinearArgs& p, uint8_t* xs, int xrow, int64_t k0, int ke) {
@@ -590,13 +795,15 @@ gam_status launch_staged(LinearArgs p, int sms, cudaStream_t s) {
 // Forms by size, measured in us (thin with one tile, thin with two, staged):
 //   16-bit, 16 x 16384 x 4096: 27.2, 19.5, 19.3; 30 x 3712 x 5888: 17.7, 11.6, 20.8; 16 x 4096 x 1024: 3.6, 3.5, 3.4
 //   16-bit, 2 x 4745 x 4224: 7.5, -, 9.4; 1 x 768 x 768: 2.4, -, 5.0
+//   16-bit, up to 8 rows (thin, shared): 8 x 16384 x 4096: 23.5, 13.9; 8 x 8192 x 8192: 26.8, 14.1; 1 x 5120 x 8192:
+//     14.3, 13.0; 1 and 8 x 6144 x 4096: 8.7, 9.0 and 9.4, 8.8; 8 x 4096 x 8192: 11.6, 12.3; 8 x 8192 x 1024: 4.9, 5.6
 //   fp32, 2 x 15083 x 3904: 36.7, 37.1, 20.3; 16 x 16384 x 4096: 77.7, 68.0, 43.1; 64 x 4096 x 4096: 76.2, 66.1, 173
 //   fp32, 7 x 6272 x 2496: 13.5, 14.9, 12.1; 5 x 1025 x 1024: 3.8, 4.9, 5.2
 template <typename T>
 gam_status launch(const LinearArgs& p, int sms, cudaStream_t s) {
   const int64_t weights = (int64_t)p.n * p.groups * 64;
   if constexpr (Elem<T>::parts == 1) {
-    if (p.rows <= 8) return launch_thin<T, 1, 1>(p, sms, s);
+    if (p.rows <= 8) return p.n > 4096 && weights >= (24 << 20) ? launch_shared<T>(p, sms, s) : launch_thin<T, 1, 1>(p, sms, s);
     return p.n < 2048 ? launch_thin<T, 2, 1>(p, sms, s) : launch_thin<T, 2, 2>(p, sms, s);
   } else {
     if (weights <= (8 << 20)) return launch_thin<T, 1, 1>(p, sms, s);

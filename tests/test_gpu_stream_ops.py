@@ -88,6 +88,32 @@ def test_linear(dtype, rows, n, k, act, bias):
     linear_check(y, xf, q, scale, b, act, dtype)
 
 
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("rows,n,k,act,bias", [
+    (1, 16385, 1536, "none", True), (3, 4100, 6208, "swish", True), (8, 4097, 24064, "none", False),
+    (7, 37890, 704, "none", True)])
+def test_linear_many_weights_few_rows(dtype, rows, n, k, act, bias):
+    """Ends of tiles, of runs of groups and of what is held of x; aligned rows, and strided ones at an odd offset."""
+    torch = _torch()
+    x, xf, q, scale, b = linear_inputs(rows + n + k, rows, n, k, dtype, bias)
+    w, s, bd = dev(gam.gam_quant_linear_pack(q)), dev(scale), None if b is None else dev(b)
+    y = gam.gam_quant_linear(x, w, s, bias=bd, act=act)
+    some = np.r_[0:40, n // 2:n // 2 + 40, n - 300:n]
+    linear_check(y[:, dev(some)], xf, q[some], scale[some], None if b is None else b[some], act, dtype)
+    xb = torch.full((rows, k + 9), float("nan"), dtype=x.dtype, device="cuda")
+    xb[:, 3:3 + k] = x
+    yb = torch.full((rows + 2, n + 5), 77.0, dtype=x.dtype, device="cuda")
+    yv = yb[1:1 + rows, 1:1 + n]
+    gam.gam_quant_linear(xb[:, 3:3 + k], w, s, bias=bd, act=act, out=yv)
+    assert torch.equal(yv, y)
+    yv.fill_(77.0)
+    assert bool((yb == 77.0).all())
+    if rows > 1:
+        x[1, 5] = float("nan")
+        got = gam.gam_quant_linear(x, w, s, bias=bd, act=act)
+        assert bool(torch.isnan(got[1]).all()) and torch.equal(got[2:], y[2:]) and torch.equal(got[0], y[0])
+
+
 @pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
 def test_linear_strided_rows_and_untouched_memory(dtype):
     """x and out inside larger buffers at an odd offset: nothing beside out's rows changes."""
