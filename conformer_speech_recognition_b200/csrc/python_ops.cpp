@@ -10,6 +10,7 @@
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <ATen/core/grad_mode.h>
 #include <ATen/ops/empty.h>
 
 #include <optional>
@@ -86,6 +87,9 @@ struct Call {
       for (int64_t v : shape) want += (want.empty() ? "" : ", ") + std::to_string(v);
       refuse(GAM_ERR_INVALID_ARG, std::string(name) + " must have shape [" + want + "]");
     }
+    if (t.requires_grad() && at::GradMode::is_enabled())
+      refuse(GAM_ERR_INVALID_ARG, std::string(name) + " requires a gradient, which this operator does not give: call it "
+                                                      "under torch.no_grad() or with detached tensors");
     if (packed ? !t.is_contiguous() : shape.back() > 1 && t.stride(-1) != 1)
       refuse(GAM_ERR_INVALID_ARG, packed ? std::string(name) + " must be contiguous"
                                          : std::string("the last dimension of ") + name + " must be contiguous");
