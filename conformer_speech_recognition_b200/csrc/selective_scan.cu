@@ -439,6 +439,11 @@ scan_kernel(const gam_scan_args p, const int sms, const bool pair) {
   // ---- lanes: the recurrence ----
   const int part = tid % L, ch = tid / L;
   auto channel = [&](int j) { return min(c0 + ch + j * CT1, p.d - 1); };  // lanes past the last channel walk along
+  // a rate for 2^x, finite: a frame past the end has a step of 0, and 0 times an infinite rate would be NaN
+  auto rate = [](float v) {
+    v *= kLog2e;
+    return isinf(v) ? copysignf(3.4e38f, v) : v;
+  };
   u64 a[CH][S / 2], h[CH][S / 2];
   int col[CH];                                       // channel j's place in a row of s_in
 #pragma unroll
@@ -448,7 +453,7 @@ scan_kernel(const gam_scan_args p, const int sms, const bool pair) {
 #pragma unroll
     for (int i = 0; i < S / 2; ++i) {
       const int k = part * S + 2 * i;
-      a[j][i] = pack2(k < p.n ? pa[k] * kLog2e : 0.f, k + 1 < p.n ? pa[k + 1] * kLog2e : 0.f);
+      a[j][i] = pack2(k < p.n ? rate(pa[k]) : 0.f, k + 1 < p.n ? rate(pa[k + 1]) : 0.f);
       h[j][i] = pack2(st && k < p.n ? st[k] : 0.f, st && k + 1 < p.n ? st[k + 1] : 0.f);
     }
     const int c = ch + j * CT1;

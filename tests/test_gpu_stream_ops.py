@@ -357,6 +357,21 @@ def test_scan_steps_of_zero_keep_the_state(dtype, B, T, d, n):
     assert torch.equal(new[:, ::3], t["state"][:, ::3]) and not torch.equal(new, t["state"])
 
 
+@pytest.mark.parametrize("dtype", ["f32", "f16"])
+@pytest.mark.parametrize("B,T,d,n", [(2, 3, 24, 8), (3, 70, 24, 8), (1, 1500, 16, 16), (40, 9, 1024, 16)])
+def test_scan_infinite_rates_forget_their_state(dtype, B, T, d, n):
+    """exp(s a) is 0 for a = -inf: such a state is its last frame's input, in ragged sequences too."""
+    torch = _torch()
+    t, f = scan_inputs(21 + T, B, T, d, n, dtype)
+    t["a"][:, 1] = float("-inf")
+    lens = [T - i % 3 for i in range(B)]
+    t["c"][..., 1] = 0
+    y, new = scan_call(t, dev(np.array(lens, np.int32)))
+    assert bool(torch.isfinite(y).all()) and bool(torch.isfinite(new).all())
+    f["a"][:, 1], f["c"][..., 1] = -1e30, 0
+    scan_check(y, new, f, lens, dtype)
+
+
 def test_scan_no_frames_hands_the_state_on():
     torch = _torch()
     t, _ = scan_inputs(10, 2, 1, 24, 7, "f32")
@@ -685,3 +700,15 @@ def test_stream_argument_and_device_checks():
     with pytest.raises(gam.GamError) as e:
         gam.gam_residual_norm(x, y[:, ::2])
     assert e.value.name == "GAM_ERR_INVALID_ARG"
+
+
+def test_tensors_that_require_gradients_are_refused():
+    torch = _torch()
+    x, y = torch.randn(3, 32, device="cuda"), torch.randn(3, 32, device="cuda")
+    w = torch.ones(32, device="cuda", requires_grad=True)
+    with pytest.raises(gam.GamError, match="pre_weight requires a gradient"):
+        gam.gam_residual_norm(x, y, pre="rms", pre_weight=w)
+    with torch.no_grad():
+        a = gam.gam_residual_norm(x, y, pre="rms", pre_weight=w)
+    b = gam.gam_residual_norm(x, y, pre="rms", pre_weight=w.detach())
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
