@@ -559,7 +559,9 @@ gam_status launch_shared(LinearArgs p, int sms, cudaStream_t s) {
   cfg.attrs = attr;
   cfg.numAttrs = R > 1 ? 1 : 0;
   auto kernel = quant_linear_shared_kernel<T>;
-  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)cfg.dynamicSmemBytes);
+  // The limit belongs to the kernel, not to the call: every call sets the same one, so that no thread lowers another's.
+  static_assert(kSharedSmem - ring >= 8 * (512 + 16), "a run of 8 rows fits");
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSharedSmem);
   if (e != cudaSuccess) return launch_status(e);
   return launch_status(cudaLaunchKernelEx(&cfg, kernel, p));
 }
