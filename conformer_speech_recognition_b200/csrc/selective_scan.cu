@@ -62,30 +62,29 @@ __device__ __forceinline__ float rcp_approx(float v) {
 }
 
 // 2^x for two values on the fp32 and integer pipes: x = n + f, n whole and |f| <= 1/2 by
-// the rounding of an addition, 2^f by the polynomial of degree 5 with 2^0 = 1 and the
-// least largest relative error (8e-8; 1.6e-7 evaluated in fp32, 6e-8 for |f| < 0.001), 2^n
-// into the exponent.  Below -125 the result stays 2^-125, which is as good as 0 beside any
-// input; 128 gives infinity; NaN stays.
+// the rounding of an addition, 2^(f+1) by the polynomial of degree 5 with 2^1 = 2 and the
+// least largest relative error (8e-8; 1.6e-7 evaluated in fp32, 6e-8 for |f| < 0.001), and a
+// product with 2^(n-1), whose exponent field is n + 126.  Below -125.5 the field is 0 and so
+// is the result; 128 gives infinity; NaN comes through the product.
 __device__ __forceinline__ float clamp_exponent(float v) {
   float r;
-  asm("{\n\t.reg .f32 t;\n\tmax.NaN.f32 t, %1, 0fC2FA0000;\n\tmin.NaN.f32 %0, t, 0f43000000;\n\t}" : "=f"(r) : "f"(v));
+  asm("{\n\t.reg .f32 t;\n\tmax.NaN.f32 t, %1, 0fC2FC0000;\n\tmin.NaN.f32 %0, t, 0f43000000;\n\t}" : "=f"(r) : "f"(v));
   return r;
 }
 __device__ __forceinline__ u64 exp2_poly2(u64 x) {
   const float2 c = unpack2(x);
   const u64 v = pack2(clamp_exponent(c.x), clamp_exponent(c.y));
   const u64 one = both(1.f);
-  const u64 t = fma2(v, one, both(12582912.f));      // 1.5 * 2^23: its last bit counts ones
-  const u64 f = fma2(fma2(t, one, both(-12582912.f)), both(-1.f), v);
-  u64 q = both(0.0013274633092805743f);
-  q = fma2(q, f, both(0.009671961888670921f));
-  q = fma2(q, f, both(0.055506784468889236f));
-  q = fma2(q, f, both(0.24022234976291656f));
-  q = fma2(q, f, both(0.6931470632553101f));
-  q = fma2(q, f, one);
-  const float2 n = unpack2(t), r = unpack2(q);
-  return pack2(__int_as_float(__float_as_int(r.x) + (__float_as_int(n.x) << 23)),
-               __int_as_float(__float_as_int(r.y) + (__float_as_int(n.y) << 23)));
+  const u64 t = fma2(v, one, both(12583038.f));      // 1.5 * 2^23 + 126: its last bit counts ones
+  const u64 f = fma2(fma2(t, one, both(-12583038.f)), both(-1.f), v);
+  u64 q = both(0.0026549266185611486f);
+  q = fma2(q, f, both(0.019343923777341843f));
+  q = fma2(q, f, both(0.11101356893777847f));
+  q = fma2(q, f, both(0.48044469952583313f));
+  q = fma2(q, f, both(1.3862941265106201f));
+  q = fma2(q, f, both(2.f));
+  const float2 n = unpack2(t);
+  return mul2(q, pack2(__int_as_float(__float_as_int(n.x) << 23), __int_as_float(__float_as_int(n.y) << 23)));
 }
 // A decay 2^(s a).  A state that decays slowly adds up the decays' errors over many frames: with the hardware's
 // 2^x (2^-22) an fp32 call's outputs came out 1e-6 off, so fp32 calls take the polynomial.  16-bit calls keep the

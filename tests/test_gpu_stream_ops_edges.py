@@ -49,3 +49,35 @@ def test_linear_calls_of_several_threads():
     assert not bad, f"{len(bad)} of {len(jobs) * calls} calls failed: {gam.STATUS[bad[0]]}"
     for _, want, y, _ in jobs:
         assert torch.equal(y, want)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("T,n", [(3, 16), (40, 16), (1500, 16), (40, 5)])
+def test_scan_nan_rate_reaches_its_channel_only(dtype, T, n):
+    """A rate that is NaN makes its channel's outputs NaN from the first valid frame on."""
+    torch = _torch()
+    t, _ = scan_inputs(31 + T, 2, T, 48, n, dtype)
+    ln = dev(np.array([T, T - 1], np.int32))
+    clean, end = scan_call(t, ln)
+    t["a"] = t["a"].clone()
+    t["a"][5, 2] = float("nan")
+    y, new = scan_call(t, ln)
+    assert bool(torch.isnan(y[0, :, 5]).all()) and bool(torch.isnan(y[1, :T - 1, 5]).all())
+    assert bool(torch.isnan(new[:, 5, 2]).all())
+    keep = torch.arange(48, device="cuda") != 5
+    assert torch.equal(y[..., keep], clean[..., keep]) and torch.equal(new[:, keep], end[:, keep])
+    others = torch.arange(n, device="cuda") != 2
+    assert torch.equal(new[:, 5, others], end[:, 5, others])
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16"])
+@pytest.mark.parametrize("T", [1, 2, 40, 1500])
+def test_scan_infinite_rates_clear_large_states(dtype, T):
+    """exp(-inf) and exp(-1e4) are 0: nothing of a state of 1e30 is left."""
+    torch = _torch()
+    t, _ = scan_inputs(32, 2, T, 24, 16, dtype)
+    t["state"] = torch.full_like(t["state"], 1e30)
+    t["x"] = torch.zeros_like(t["x"])
+    t["a"][:, 1], t["a"][:, 2] = float("-inf"), -1e8
+    _, new = scan_call(t)
+    assert bool((new[..., 1:3] == 0).all())
