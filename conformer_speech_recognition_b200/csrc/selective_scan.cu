@@ -573,7 +573,8 @@ scan_kernel(const gam_scan_args p, const int sms, const bool pair) {
     }
     cluster.sync();
     if (rank > 0) {
-      for (int r = 0; r < rank; ++r) {
+      // a piece without frames changes nothing, not even by a decay of 0 times an infinite or NaN rate
+      for (int r = 0; r < rank && (r == 0 || r * piece < len); ++r) {
         const float* e = s_join + r * JOIN;
 #pragma unroll
         for (int j = 0; j < CH; ++j) {

@@ -81,3 +81,15 @@ def test_scan_infinite_rates_clear_large_states(dtype, T):
     t["a"][:, 1], t["a"][:, 2] = float("-inf"), -1e8
     _, new = scan_call(t)
     assert bool((new[..., 1:3] == 0).all())
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("T", [3, 40, 1500])
+def test_scan_sequences_without_frames_keep_their_states(dtype, T):
+    """Whatever the rates are: NaN here, and 0 times infinity where a step of 0 meets an infinite one."""
+    torch = _torch()
+    t, _ = scan_inputs(39 + T, 3, T, 48, 16, dtype)
+    t["a"] = t["a"].clone()
+    t["a"][5, 2], t["a"][6, 3] = float("nan"), float("-inf")
+    _, new = scan_call(t, dev(np.array([T, 0, -1], np.int32)))
+    assert torch.equal(new[1:], t["state"][1:])
