@@ -99,6 +99,14 @@ __device__ __forceinline__ u64 decay2(u64 s, u64 a) {
   else return exp2_approx2(fma2(s, a, both(kRaise)));
 }
 
+// An infinite rate stands for the largest finite one: a step of 0, as behind a sequence's end, then keeps the
+// state, where 0 times infinity would be NaN.
+__device__ __forceinline__ float finite_rate(float v) {
+  float r;
+  asm("{\n\t.reg .f32 t;\n\tmax.NaN.f32 t, %1, 0fFF7FFFFF;\n\tmin.NaN.f32 %0, t, 0f7F7FFFFF;\n\t}" : "=f"(r) : "f"(v));
+  return r;
+}
+
 // log(1 + e^v) = max(v, 0) + log1p(e), e = e^-|v| in (0, 1], for two values.  log1p(e) / e
 // by the polynomial of degree 8 with the least largest relative error on [0, 1] (3e-8;
 // 1.7e-7 evaluated in fp32): nothing cancels, so small steps keep their digits.
@@ -438,11 +446,7 @@ scan_kernel(const gam_scan_args p, const int sms, const bool pair) {
   // ---- lanes: the recurrence ----
   const int part = tid % L, ch = tid / L;
   auto channel = [&](int j) { return min(c0 + ch + j * CT1, p.d - 1); };  // lanes past the last channel walk along
-  // a rate for 2^x, finite: a frame past the end has a step of 0, and 0 times an infinite rate would be NaN
-  auto rate = [](float v) {
-    v *= kLog2e;
-    return isinf(v) ? copysignf(3.4e38f, v) : v;
-  };
+  auto rate = [](float v) { return finite_rate(v * kLog2e); };  // for 2^x
   u64 a[CH][S / 2], h[CH][S / 2];
   int col[CH];                                       // channel j's place in a row of s_in
 #pragma unroll
@@ -699,7 +703,8 @@ __global__ void __launch_bounds__(256) step_kernel(const gam_scan_args p) {
       float v = 0.f;
 #pragma unroll
       for (int i = 0; i < 4; i += 2) {
-        const float2 decay = unpack2(decay2<T>(both(e), pack2(a[j][i], a[j][i + 1])));
+        // the rates are bounded here, not where they are loaded: the loads of the frame would wait for them (+0.5 us)
+        const float2 decay = unpack2(decay2<T>(both(e), pack2(finite_rate(a[j][i]), finite_rate(a[j][i + 1]))));
         h[j][i] = fmaf(decay.x, h[j][i], sx * bv[i]);
         h[j][i + 1] = fmaf(decay.y, h[j][i + 1], sx * bv[i + 1]);
         v = fmaf(cv[i], h[j][i], v);

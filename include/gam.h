@@ -441,7 +441,8 @@ typedef struct {
  *   s   = softplus(dt[t, c] + dt_bias[c])     (or without softplus)
  *   h_i = exp(s a[c, i]) h_i + s x[t, c] b[t, i]
  *   y[t, c] = (sum_i c[t, i] h_i + d_skip[c] x[t, c]) * z sigmoid(z),  z = z[t, c]
- * n is 1 .. 64 (GAM_ERR_SHAPE).  Frames at or beyond a sequence's length are
+ * n is 1 .. 64 (GAM_ERR_SHAPE).  An infinite rate stands for the largest finite
+ * one of its sign: a step of 0 keeps every state.  Frames at or beyond a sequence's length are
  * never read, leave the state alone and are written as zeros in y.  Arguments
  * are DEVICE pointers in a HOST struct, which the call does not keep. */
 gam_status gam_selective_scan(const gam_scan_args* args, void* stream);

@@ -93,3 +93,20 @@ def test_scan_sequences_without_frames_keep_their_states(dtype, T):
     t["a"][5, 2], t["a"][6, 3] = float("nan"), float("-inf")
     _, new = scan_call(t, dev(np.array([T, 0, -1], np.int32)))
     assert torch.equal(new[1:], t["state"][1:])
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("T", [1, 4, 5, 40, 1500])
+def test_scan_steps_of_zero_keep_states_of_infinite_rates(dtype, T):
+    """An infinite rate stands for the largest finite one, so a step of 0 keeps the state, in prompts and frames alike."""
+    torch = _torch()
+    t, _ = scan_inputs(33 + T, 2, T, 24, 16, dtype)
+    t["a"] = t["a"].clone()
+    t["a"][:, 1], t["a"][:, 3] = float("-inf"), float("inf")
+    t["dt"], t["dt_bias"] = torch.zeros_like(t["dt"]), None
+    y, new = scan_call(t, dt_softplus=False)
+    assert torch.equal(new, t["state"]) and bool(torch.isfinite(y).all())
+    t["a"][:, 3] = -1.0
+    t["dt"] = torch.full_like(t["dt"], -200.0)         # its softplus is below the smallest fp32 number
+    y, new = scan_call(t)
+    assert torch.equal(new, t["state"]) and bool(torch.isfinite(y).all())
