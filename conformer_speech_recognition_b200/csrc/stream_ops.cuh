@@ -1,5 +1,5 @@
 // Shared pieces of the streaming-block operators (quant_linear.cu, short_conv.cu,
-// selective_scan.cu, residual_norm.cu): element types, activations and the
+// selective_scan.cuh, residual_norm.cu): element types, activations and the
 // checks that every call makes before its launch.
 #pragma once
 
