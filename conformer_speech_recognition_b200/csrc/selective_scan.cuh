@@ -243,7 +243,10 @@ struct ScanShape {
   }
 };
 
-template <typename T, int S, int L, int CH, bool WIDE>
+// States past n: with an infinite s x they would be infinity times b = 0, a NaN that reaches y through c = 0.  A lane
+// that has no others adds 0 to y; where a lane has some of both kinds (PAD: n no multiple of S) they are put back to
+// 0 after every frame.
+template <typename T, int S, int L, int CH, bool WIDE, bool PAD>
 __global__ void __launch_bounds__(ScanShape<T, S, L, CH>::THREADS, ScanShape<T, S, L, CH>::SPLIT ? 6 : 8)
 scan_kernel(const gam_scan_args p, const int sms, const bool pair) {
   using Shape = ScanShape<T, S, L, CH>;
@@ -448,6 +451,7 @@ scan_kernel(const gam_scan_args p, const int sms, const bool pair) {
 
   // ---- lanes: the recurrence ----
   const int part = tid % L, ch = tid / L;
+  const int valid = p.n - part * S;                  // of this lane's states
   auto channel = [&](int j) { return min(c0 + ch + j * CT1, p.d - 1); };  // lanes past the last channel walk along
   auto rate = [](float v) { return finite_rate(v * kLog2e); };  // for 2^x
   u64 a[CH][S / 2], h[CH][S / 2];
@@ -495,6 +499,10 @@ scan_kernel(const gam_scan_args p, const int sms, const bool pair) {
                 u64& hh = h[j][2 * i + q];
                 const u64 decay = decay2<T>(s2[j], a[j][2 * i + q]);
                 hh = fma2(decay, hh, mul2(sx2[j], q ? bv.y : bv.x));
+                if constexpr (PAD) {
+                  const float2 v = unpack2(hh);
+                  hh = pack2(4 * i + 2 * q < valid ? v.x : 0.f, 4 * i + 2 * q + 1 < valid ? v.y : 0.f);
+                }
                 if (OUT) y2[j] = i + q ? fma2(q ? cv.y : cv.x, hh, y2[j]) : mul2(cv.x, hh);
               }
           }
@@ -502,7 +510,7 @@ scan_kernel(const gam_scan_args p, const int sms, const bool pair) {
 #pragma unroll
             for (int j = 0; j < CH; ++j) {
               const float2 yy = unpack2(y2[j]);
-              v[j][f] = yy.x + yy.y;
+              v[j][f] = L == 1 || valid > 0 ? yy.x + yy.y : 0.f;
             }
         }
         if constexpr (OUT) {
@@ -710,9 +718,14 @@ __global__ void __launch_bounds__(256) step_kernel(const gam_scan_args p) {
         const float2 decay = unpack2(decay2<T>(both(e), pack2(finite_rate(a[j][i]), finite_rate(a[j][i + 1]))));
         h[j][i] = fmaf(decay.x, h[j][i], sx * bv[i]);
         h[j][i + 1] = fmaf(decay.y, h[j][i + 1], sx * bv[i + 1]);
+        if constexpr (!VEC) {                          // states past n stay 0 whatever s x is
+          if (k0 + i >= p.n) h[j][i] = 0.f;
+          if (k0 + i + 1 >= p.n) h[j][i + 1] = 0.f;
+        }
         v = fmaf(cv[i], h[j][i], v);
         v = fmaf(cv[i + 1], h[j][i + 1], v);
       }
+      if (VEC && k0 >= p.n) v = 0.f;
 #pragma unroll
       for (int o = L / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
       v = fmaf(skip[j], xv, v);
@@ -786,7 +799,9 @@ gam_status launch_scan(const gam_scan_args& p, int sms, cudaStream_t s) {
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = R > 1 ? 1 : 0;
-  auto kernel = wide ? scan_kernel<T, S, L, CH, true> : scan_kernel<T, S, L, CH, false>;
+  const bool pad = p.n % S != 0;
+  auto kernel = wide ? (pad ? scan_kernel<T, S, L, CH, true, true> : scan_kernel<T, S, L, CH, true, false>)
+                     : (pad ? scan_kernel<T, S, L, CH, false, true> : scan_kernel<T, S, L, CH, false, false>);
   if (cfg.dynamicSmemBytes + CT * 8 + 64 > 48 * 1024) {  // with the static part
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)cfg.dynamicSmemBytes);
     if (e != cudaSuccess) return launch_status(e);

@@ -110,3 +110,27 @@ def test_scan_steps_of_zero_keep_states_of_infinite_rates(dtype, T):
     t["dt"] = torch.full_like(t["dt"], -200.0)         # its softplus is below the smallest fp32 number
     y, new = scan_call(t)
     assert torch.equal(new, t["state"]) and bool(torch.isfinite(y).all())
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("B,T,d,n", [(2, 3, 24, 1), (2, 3, 33, 5), (2, 4, 24, 12), (2, 40, 24, 1), (2, 40, 33, 5), (2, 40, 24, 12),
+                                     (1, 700, 24, 5), (1, 700, 24, 12), (2, 40, 24, 16), (2, 40, 24, 33), (64, 20, 1272, 7),
+                                     (64, 20, 640, 12)])
+def test_scan_infinite_inputs_do_not_depend_on_the_padding_of_n(dtype, B, T, d, n):
+    """An infinite x makes its channel's states and outputs infinite from its frame on, whatever n is."""
+    torch = _torch()
+    t, _ = scan_inputs(34 + T + n, B, T, d, n, dtype, z=False)
+    t["b"], t["c"] = t["b"].abs() + 0.25, t["c"].abs() + 0.25
+    t["d_skip"] = t["d_skip"].abs() + 0.25
+    t["a"] = t["a"].clamp(min=-2.0)                    # no decay is 0
+    clean, end = scan_call(t)
+    t["x"] = t["x"].clone()
+    at = T // 2
+    t["x"][0, at, 3] = float("inf")
+    y, new = scan_call(t)
+    hurt = torch.zeros_like(y, dtype=torch.bool)
+    hurt[0, at:, 3] = True
+    assert bool((y[hurt] == float("inf")).all()) and torch.equal(y[~hurt], clean[~hurt])
+    assert bool((new[0, 3] == float("inf")).all())
+    new[0, 3] = end[0, 3]
+    assert torch.equal(new, end)
