@@ -102,6 +102,20 @@ __device__ __forceinline__ u64 decay2(u64 s, u64 a) {
   else return exp2_approx2(fma2(s, a, both(kRaise)));
 }
 
+// h 2^(q a) where the exponent sums up many frames and may leave fp32's range although h 2^(q a) does not: beyond
+// 2^+-120 it goes in two halves.  A state of 0 or of infinity stays what it is, as it does frame by frame.
+template <typename T>
+__device__ __forceinline__ u64 carry2(u64 h, float q, u64 a) {
+  const float2 r = unpack2(a), v = unpack2(h);
+  const bool far = fmaxf(fabsf(q * r.x), fabsf(q * r.y)) > 120.f;
+  const u64 decay = decay2<T>(both(far ? 0.5f * q : q), a);
+  u64 w = mul2(h, decay);
+  if (far) w = mul2(w, decay);
+  const float2 u = unpack2(w);
+  auto rigid = [](float x) { return x == 0.f || isinf(x); };
+  return pack2(rigid(v.x) ? v.x : u.x, rigid(v.y) ? v.y : u.y);
+}
+
 // An infinite rate stands for the largest finite one: a step of 0, as behind a sequence's end, then keeps the
 // state, where 0 times infinity would be NaN.
 __device__ __forceinline__ float finite_rate(float v) {
@@ -601,9 +615,8 @@ scan_kernel(const gam_scan_args p, const int sms, const bool pair) {
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
               u64& hh = h[j][2 * i + k];
-              const u64 decay = decay2<T>(both(q), a[j][2 * i + k]);
               // the first piece's end state is whole already
-              hh = r ? fma2(decay, hh, k ? end.y : end.x) : (k ? end.y : end.x);
+              hh = r ? fma2(both(1.f), carry2<T>(hh, q, a[j][2 * i + k]), k ? end.y : end.x) : (k ? end.y : end.x);
             }
           }
         }

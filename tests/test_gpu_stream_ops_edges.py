@@ -134,3 +134,37 @@ def test_scan_infinite_inputs_do_not_depend_on_the_padding_of_n(dtype, B, T, d, 
     assert bool((new[0, 3] == float("inf")).all())
     new[0, 3] = end[0, 3]
     assert torch.equal(new, end)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+def test_scan_growing_states_of_long_prompts(dtype):
+    """Rates above 0: a product of decays may pass fp32's range where the states do not."""
+    torch = _torch()
+    # states that grow, but are 0 until the last frames
+    t, f = scan_inputs(35, 1, 1500, 16, 16, dtype, state=False)
+    for name in ("x", "dt", "dt_bias", "a"):
+        t[name] = t[name].clone()
+    t["x"][:, :-5] = 0
+    t["dt"][:], t["dt_bias"][:] = 0.5, 0
+    t["a"][:, :3] = 1.0
+    f.update({name: host(t[name]) for name in ("x", "dt", "dt_bias", "a")})
+    y, new = scan_call(t, dt_softplus=False)
+    scan_check(y, new, f, [1500], dtype, softplus=False)
+    # a state of 1e-37 that grows by e^93 within 64 frames
+    t, f = scan_inputs(36, 1, 512, 16, 16, dtype)
+    for name in ("x", "dt", "dt_bias", "a", "state"):
+        t[name] = t[name].clone()
+    t["x"][:], t["dt"][:], t["dt_bias"][:] = 0, 0, 0
+    t["dt"][:, 64:128] = 1.453125
+    t["a"][:, 0], t["state"][:] = 1.0, 1e-37
+    f.update({name: host(t[name]) for name in ("x", "dt", "dt_bias", "a", "state")})
+    y, new = scan_call(t, dt_softplus=False)
+    scan_check(y, new, f, [512], dtype, softplus=False)
+    assert bool((new[..., 0] > 100).all())
+    # an infinite state stays infinite under decays whose product is too small for fp32
+    t, _ = scan_inputs(37, 1, 1500, 16, 16, dtype)
+    t["x"] = t["x"].clone()
+    t["x"][0, 2, 3] = float("inf")
+    t["dt"], t["dt_bias"] = torch.full_like(t["dt"], 0.5), None
+    _, new = scan_call(t, dt_softplus=False)
+    assert bool(torch.isinf(new[0, 3]).all())
