@@ -318,7 +318,7 @@ __global__ void __launch_bounds__(kThinWarps * 32, NT > 1 ? 2 : 3) quant_linear_
     for (int q = 1; q < R; ++q) v += join[(q - 1) * outs + i];
     v *= kUnpackScale<M>;
     if (p.bias) v += p.bias[o];
-    ((T*)p.y)[m * p.ldy + o] = from_f<T>(p.act == GAM_ACT_SWISH ? swish_f(v) : v);
+    ((T*)p.y)[m * p.ldy + o] = from_f<T>(p.act == GAM_ACT_SWISH ? swish_f<T>(v) : v);
   }
 }
 
@@ -533,7 +533,7 @@ __global__ void __launch_bounds__(kSharedWarps * 32, 2) quant_linear_shared_kern
       for (int e = 0; e < 2; ++e) {
         const int r = 2 * t + e;
         const float v = (e ? sums.y : sums.x) * kUnpackScale<T> + bias;
-        if (r < p.rows) ((T*)p.y)[r * p.ldy + o] = from_f<T>(p.act == GAM_ACT_SWISH ? swish_f(v) : v);
+        if (r < p.rows) ((T*)p.y)[r * p.ldy + o] = from_f<T>(p.act == GAM_ACT_SWISH ? swish_f<T>(v) : v);
       }
     }
 }
@@ -769,7 +769,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) quant_linear_staged_kernel(con
       float v = sum(i);
       v *= kUnpackScale<M>;
       if (p.bias) v += p.bias[o];
-      ((float*)p.y)[m * p.ldy + o] = p.act == GAM_ACT_SWISH ? swish_f(v) : v;
+      ((float*)p.y)[m * p.ldy + o] = p.act == GAM_ACT_SWISH ? swish_f<float>(v) : v;
     }
     __syncthreads();
   }

@@ -208,9 +208,27 @@ residual_norm_kernel(const gam_residual_norm_args p, const int64_t per_gate) {
 #pragma unroll
           for (int i = 0; i < V; ++i) y[j][i] *= act(g[j][i]);
       };
+      auto gate2 = [&](auto act) {                     // of pairs (a single value in both halves)
+        constexpr int B = V > 1 ? 1 : 0;
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+#pragma unroll
+          for (int i = 0; i < V; i += 2) {
+            const float2 f = unpack2(act(pack2(g[j][i], g[j][i + B])));
+            y[j][i] *= f.x;
+            if constexpr (V > 1) y[j][i + 1] *= f.y;
+          }
+      };
+      constexpr bool F32 = sizeof(TX) == 4;            // a factor of the residual: in its type's precision
       switch (p.gate_act) {
-        case GAM_ACT_SWISH: gate([](float v) { return swish_f(v); }); break;
-        case GAM_ACT_SIGMOID: gate([](float v) { return sigmoid_f(v); }); break;
+        case GAM_ACT_SWISH:
+          if constexpr (F32) gate2([](u64 v) { return swish2(v); });
+          else gate([](float v) { return swish_f<TX>(v); });
+          break;
+        case GAM_ACT_SIGMOID:
+          if constexpr (F32) gate2([](u64 v) { return sigmoid2(v); });
+          else gate([](float v) { return sigmoid_f<TX>(v); });
+          break;
         case GAM_ACT_TANH: gate([](float v) { return tanhf(v); }); break;
         default: gate([](float v) { return v; });
       }

@@ -48,35 +48,19 @@ namespace {
 
 namespace cg = cooperative_groups;
 
+// a lambda left as a call would keep the states it refers to in local memory (three times the time)
+#define GAM_INLINE __attribute__((always_inline))
+
 constexpr float kLog2e = 1.4426950408889634f;
-__device__ __forceinline__ float exp2_approx(float v) {
-  float r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
-  return r;
-}
-__device__ __forceinline__ u64 exp2_approx2(u64 v) {
-  const float2 e = unpack2(v);
-  return pack2(exp2_approx(e.x), exp2_approx(e.y));
-}
-__device__ __forceinline__ float rcp_approx(float v) {
-  float r;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
-  return r;
-}
 
 // 2^x for two values on the fp32 and integer pipes: x = n + f, n whole and |f| <= 1/2 by
 // the rounding of an addition, 2^(f+1) by the polynomial of degree 5 with 2^1 = 2 and the
 // least largest relative error (8e-8; 1.6e-7 evaluated in fp32, 6e-8 for |f| < 0.001), and a
 // product with 2^(n-1), whose exponent field is n + 126.  Below -125.5 the field is 0 and so
 // is the result; 128 gives infinity; NaN comes through the product.
-__device__ __forceinline__ float clamp_exponent(float v) {
-  float r;
-  asm("{\n\t.reg .f32 t;\n\tmax.NaN.f32 t, %1, 0fC2FC0000;\n\tmin.NaN.f32 %0, t, 0f43000000;\n\t}" : "=f"(r) : "f"(v));
-  return r;
-}
 __device__ __forceinline__ u64 exp2_poly2(u64 x) {
   const float2 c = unpack2(x);
-  const u64 v = pack2(clamp_exponent(c.x), clamp_exponent(c.y));
+  const u64 v = pack2(clamp_f(c.x, -126.f, 128.f), clamp_f(c.y, -126.f, 128.f));
   const u64 one = both(1.f);
   const u64 t = fma2(v, one, both(12583038.f));      // 1.5 * 2^23 + 126: its last bit counts ones
   const u64 f = fma2(fma2(t, one, both(-12583038.f)), both(-1.f), v);
@@ -118,11 +102,7 @@ __device__ __forceinline__ u64 carry2(u64 h, float q, u64 a) {
 
 // An infinite rate stands for the largest finite one: a step of 0, as behind a sequence's end, then keeps the
 // state, where 0 times infinity would be NaN.
-__device__ __forceinline__ float finite_rate(float v) {
-  float r;
-  asm("{\n\t.reg .f32 t;\n\tmax.NaN.f32 t, %1, 0fFF7FFFFF;\n\tmin.NaN.f32 %0, t, 0f7F7FFFFF;\n\t}" : "=f"(r) : "f"(v));
-  return r;
-}
+__device__ __forceinline__ float finite_rate(float v) { return clamp_f(v, -3.4028235e38f, 3.4028235e38f); }
 
 // log(1 + e^v) = max(v, 0) + log1p(e), e = e^-|v| in (0, 1], for two values.  log1p(e) / e
 // by the polynomial of degree 8 with the least largest relative error on [0, 1] (3e-8;
@@ -141,7 +121,6 @@ __device__ __forceinline__ float2 softplus2(float2 v) {
   q = fma2(q, e, both(0.9999999403953552f));
   return unpack2(fma2(q, e, pack2(fmaxf(v.x, 0.f), fmaxf(v.y, 0.f))));
 }
-__device__ __forceinline__ float gate_f(float z) { return z * rcp_approx(1.f + exp2_approx(-z * kLog2e)); }
 
 __device__ __forceinline__ int length_of(const gam_scan_args& p, int b) {
   return p.lengths ? min(max(p.lengths[b], 0), p.t_max) : p.t_max;
@@ -327,7 +306,7 @@ scan_kernel(const gam_scan_args p, const int sms, const bool pair) {
     const T* pb = (const T*)p.b + b * p.b_batch_stride;
     const T* pc = (const T*)p.c + b * p.c_batch_stride;
     T* py = (T*)p.y + b * p.y_batch_stride + at;
-    auto fetch = [&](auto out_tag, int k) {          // tile k on its way
+    auto fetch = [&](auto out_tag, int k) GAM_INLINE {          // tile k on its way
         constexpr bool OUT = decltype(out_tag)::value;
         const int t0 = lo + k * TT, t = t0 + tt;
         if (k < tiles) {
@@ -358,7 +337,7 @@ scan_kernel(const gam_scan_args p, const int sms, const bool pair) {
         else r.load(g, mine && lo + k * TT + tt < hi, left);
         return r;
       };
-      auto prepare = [&](auto out_tag, int k) {      // s, s x, b and c of tile k
+      auto prepare = [&](auto out_tag, int k) GAM_INLINE {      // s, s x, b and c of tile k
         constexpr bool OUT = decltype(out_tag)::value;
         const int t0 = lo + k * TT, t = t0 + tt;
         if (tt < TT) {
@@ -398,7 +377,7 @@ scan_kernel(const gam_scan_args p, const int sms, const bool pair) {
           }
         }
       };
-      auto finish = [&](int k) {                     // skip and gate, and out
+      auto finish = [&](int k) GAM_INLINE {                     // skip and gate, and out
         const int t = lo + k * TT + tt;
         if (!mine || t >= hi) return;
         const Octet<T, WIDE> x = octet(k, 0, px + t * p.x_row_stride);
@@ -408,7 +387,14 @@ scan_kernel(const gam_scan_args p, const int sms, const bool pair) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           o[i] = fmaf(s_skip[o8 * 8 + i], x.get(i), s_y[k & 1][tt][o8 * 8 + i]);
-          if (pz) o[i] *= gate_f(z.get(i));
+          if (sizeof(T) == 2 && pz) o[i] *= swish_f<T>(z.get(i));
+        }
+        if (sizeof(T) == 4 && pz) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float2 g = unpack2(swish2(pack2(z.get(2 * i), z.get(2 * i + 1))));
+            o[2 * i] *= g.x, o[2 * i + 1] *= g.y;
+          }
         }
         T* dst = py + t * p.y_row_stride;
         if constexpr (WIDE) {
@@ -434,7 +420,7 @@ scan_kernel(const gam_scan_args p, const int sms, const bool pair) {
     };
     if (SPLIT && threadIdx.x >= kLanes) {
       // while the lanes run tile k: the y of the one before goes out, the one after is made ready
-      auto pass = [&](auto out_tag, bool joined) {
+      auto pass = [&](auto out_tag, bool joined) GAM_INLINE {
         constexpr bool OUT = decltype(out_tag)::value;
         fetch(out_tag, 0);
         fetch(out_tag, 1);
@@ -485,7 +471,7 @@ scan_kernel(const gam_scan_args p, const int sms, const bool pair) {
   }
   float sum_s[CH] = {};
   // The lanes' work on tile k; OUT: with outputs, else for the end state and the sum of s alone.
-  auto run = [&](auto out_tag, int k) {
+  auto run = [&](auto out_tag, int k) GAM_INLINE {
     constexpr bool OUT = decltype(out_tag)::value;
     const int buf = k & 1;
 #pragma unroll 1
@@ -558,7 +544,7 @@ scan_kernel(const gam_scan_args p, const int sms, const bool pair) {
   };
   // One run over the piece.  Without producers a thread does both: it prepares the next tile before it
   // runs this one, so that one barrier a tile is enough and the warps of a CTA need not go in step.
-  auto pass = [&](auto out_tag) {
+  auto pass = [&](auto out_tag) GAM_INLINE {
     constexpr bool OUT = decltype(out_tag)::value;
     if constexpr (SPLIT) {
       __syncthreads();                               // the first tile is there
@@ -742,7 +728,7 @@ __global__ void __launch_bounds__(256) step_kernel(const gam_scan_args p) {
 #pragma unroll
       for (int o = L / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
       v = fmaf(skip[j], xv, v);
-      if (pz) v *= gate_f(from_bits<T>(uz[j]));
+      if (pz) v *= swish_f<T>(from_bits<T>(uz[j]));
       if (c0 + j * CT < p.d && part == 0) y[t * p.y_row_stride + ch[j]] = from_f<T>(v);
     }
   }
@@ -846,6 +832,8 @@ gam_status launch(const gam_scan_args& p, int sms, cudaStream_t s) {
   if (p.n <= 32) return launch_pair<T, 8, 4, 4, 8>(p, sms, s);
   return launch_pair<T, 8, 8, 8, 8>(p, sms, s);
 }
+
+#undef GAM_INLINE
 
 }  // namespace
 }  // namespace ops

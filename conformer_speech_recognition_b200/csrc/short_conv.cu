@@ -113,9 +113,13 @@ __global__ void __launch_bounds__(kThreads) short_conv_kernel(const ConvArgs p) 
 #pragma unroll
           for (int j = 0; j + 1 < H; ++j) v[j][i] = v[j + 1][i];
           v[H - 1][i] = cur;
+          const bool swish = p.act == GAM_ACT_SWISH;
+          if constexpr (sizeof(T) == 4) {
+            if (swish) acc = swish2(acc);
+          }
           const float2 q = unpack2(acc);
-          out[2 * i] = p.act == GAM_ACT_SWISH ? swish_f(q.x) : q.x;
-          if constexpr (V > 1) out[2 * i + 1] = p.act == GAM_ACT_SWISH ? swish_f(q.y) : q.y;
+          out[2 * i] = sizeof(T) == 2 && swish ? swish_f<T>(q.x) : q.x;
+          if constexpr (V > 1) out[2 * i + 1] = sizeof(T) == 2 && swish ? swish_f<T>(q.y) : q.y;
         }
         if (t + r < tv) {
           Row o;

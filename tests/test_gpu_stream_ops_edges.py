@@ -168,3 +168,58 @@ def test_scan_growing_states_of_long_prompts(dtype):
     t["dt"], t["dt_bias"] = torch.full_like(t["dt"], 0.5), None
     _, new = scan_call(t, dt_softplus=False)
     assert bool(torch.isinf(new[0, 3]).all())
+
+
+# ---- activations in fp32 -------------------------------------------------------------
+
+# v / (1 + e^-v): the hardware's 2^x is within 2^-22 (4 u), the factor that corrects its argument and the product
+# with it add u each, the sum u, the hardware's reciprocal 2^-23 (2 u), the last product u: 10 u
+GATE = 10 * U
+
+
+def _swept(dtype, rows, d, lo=-86.0, hi=30.0):
+    t = dev(np.linspace(lo, hi, rows * d, dtype=np.float32).reshape(rows, d), _dt(dtype))
+    return t, host(t)
+
+
+def test_conv_swish_keeps_fp32():
+    v, f = _swept("f32", 96, 40)
+    w = dev(np.tile(np.array([0, 0, 1], np.float32), (40, 1)))
+    y, _ = gam.gam_short_conv(v[None], w, act="swish")
+    ref = oracle.op_activation(f, "swish")
+    inside(y[0], ref, GATE * np.abs(ref))
+
+
+def test_linear_swish_keeps_fp32():
+    """The identity as weights: each product is x or 0."""
+    torch = _torch()
+    v, f = _swept("f32", 7, 64)
+    w, s = dev(gam.gam_quant_linear_pack(np.eye(64, dtype=np.int8))), torch.ones(64, 1, dtype=torch.float16, device="cuda")
+    y = gam.gam_quant_linear(v, w, s, act="swish")
+    ref = oracle.op_activation(f, "swish")
+    inside(y, ref, GATE * np.abs(ref))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("act", ["swish", "sigmoid"])
+@pytest.mark.parametrize("rows,d", [(5, 64), (7, 201), (3, 1024)])
+def test_norm_gate_keeps_fp32(dtype, act, rows, d):
+    """x' = 0 + gate: fp32 whatever the gate's type."""
+    torch = _torch()
+    g, f = _swept(dtype, rows, d)
+    x, y = torch.zeros(rows, d, device="cuda"), torch.ones(rows, d, dtype=_dt(dtype), device="cuda")
+    xo, _ = gam.gam_residual_norm(x, y, gate=g, gate_act=act)
+    ref = oracle.op_activation(f, act)
+    inside(xo, ref, GATE * np.abs(ref))
+
+
+@pytest.mark.parametrize("T,d", [(3, 40), (70, 40), (70, 33)])
+def test_scan_gate_keeps_fp32(T, d):
+    """No state and a skip of 1: the outputs are swish(z)."""
+    torch = _torch()
+    z, f = _swept("f32", T, d)
+    one, zero = torch.ones(1, T, d, device="cuda"), torch.zeros(1, T, 4, device="cuda")
+    y, _ = gam.gam_selective_scan(one, one, -torch.ones(d, 4, device="cuda"), zero, zero, d_skip=torch.ones(d, device="cuda"),
+                                  z=z[None])
+    ref = oracle.op_activation(f, "swish")
+    inside(y[0], ref, GATE * np.abs(ref))
