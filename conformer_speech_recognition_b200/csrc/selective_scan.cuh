@@ -104,12 +104,17 @@ __device__ __forceinline__ u64 carry2(u64 h, float q, u64 a) {
 // state, where 0 times infinity would be NaN.
 __device__ __forceinline__ float finite_rate(float v) { return clamp_f(v, -3.4028235e38f, 3.4028235e38f); }
 
-// log(1 + e^v) = max(v, 0) + log1p(e), e = e^-|v| in (0, 1], for two values.  log1p(e) / e
-// by the polynomial of degree 8 with the least largest relative error on [0, 1] (3e-8;
-// 1.7e-7 evaluated in fp32): nothing cancels, so small steps keep their digits.
-// A NaN comes through e.
+// log(1 + e^v) = max(v, 0) + log1p(e), e = e^-|v| in (0, 1], for two values; fp32 in every type, since the states
+// are.  log1p(e) / e by the polynomial of degree 8 with the least largest relative error on [0, 1] (3e-8; 1.7e-7
+// evaluated in fp32): nothing cancels, so small steps keep their digits.  With e within 6 u and the last product
+// at most 9 u = 5.4e-7 off.  A NaN comes through e.
 __device__ __forceinline__ float2 softplus2(float2 v) {
-  const u64 e = pack2(exp2_approx(-fabsf(v.x) * kLog2e), exp2_approx(-fabsf(v.y) * kLog2e));
+  auto down = [](float w) {  // -|w|, -200 at least
+    float r;
+    asm("max.NaN.f32 %0, %1, 0fC3480000;" : "=f"(r) : "f"(-fabsf(w)));
+    return r;
+  };
+  const u64 e = exp2v(pack2(down(v.x), down(v.y)));
   u64 q = both(0.0052326930941379795f);
   q = fma2(q, e, both(-0.02950523979961872f));
   q = fma2(q, e, both(0.07822595536708832f));

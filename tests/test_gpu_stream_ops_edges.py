@@ -223,3 +223,18 @@ def test_scan_gate_keeps_fp32(T, d):
                                   z=z[None])
     ref = oracle.op_activation(f, "swish")
     inside(y[0], ref, GATE * np.abs(ref))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("T,d", [(2, 2048), (40, 2048), (40, 2047)])
+def test_scan_step_sizes_keep_fp32(dtype, T, d):
+    """The state after one input of 1 is softplus(dt), fp32 in every type: e^-|v| within 2 steps (4 u), the
+    polynomial 3 u with its evaluation, the last product u, and u to spare: 9 u."""
+    torch = _torch()
+    dt, f = _swept(dtype, 1, d, -80.0, 30.0)
+    x = torch.zeros(1, T, d, dtype=dt.dtype, device="cuda")
+    x[:, T - 2] = 1
+    one = torch.ones(1, T, 1, dtype=dt.dtype, device="cuda")
+    _, new = gam.gam_selective_scan(x, dt.expand(1, T, d).contiguous(), torch.zeros(d, 1, device="cuda"), one, one)
+    ref = np.logaddexp(0, f[0])
+    inside(new[0, :, 0], ref, 9 * U * ref)
