@@ -11,6 +11,7 @@
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <ATen/core/grad_mode.h>
+#include <c10/core/AutogradState.h>
 #include <ATen/ops/empty.h>
 
 #include <optional>
@@ -87,6 +88,10 @@ struct Call {
       for (int64_t v : shape) want += (want.empty() ? "" : ", ") + std::to_string(v);
       refuse(GAM_ERR_INVALID_ARG, std::string(name) + " must have shape [" + want + "]");
     }
+    // a forward-mode tangent does not make a tensor require a gradient, and no_grad does not switch it off
+    if (c10::AutogradState::get_tls_state().get_fw_grad_mode() && t._fw_grad(0).defined())
+      refuse(GAM_ERR_INVALID_ARG, std::string(name) + " carries a forward-mode gradient, which this operator does not "
+                                                      "pass on: call it with detached tensors");
     if (t.requires_grad() && at::GradMode::is_enabled())
       refuse(GAM_ERR_INVALID_ARG, std::string(name) + " requires a gradient, which this operator does not give: call it "
                                                       "under torch.no_grad() or with detached tensors");

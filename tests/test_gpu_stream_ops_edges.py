@@ -238,3 +238,19 @@ def test_scan_step_sizes_keep_fp32(dtype, T, d):
     _, new = gam.gam_selective_scan(x, dt.expand(1, T, d).contiguous(), torch.zeros(d, 1, device="cuda"), one, one)
     ref = np.logaddexp(0, f[0])
     inside(new[0, :, 0], ref, 9 * U * ref)
+
+
+# ---- what autograd sees --------------------------------------------------------------
+
+def test_forward_mode_tangents_are_refused():
+    torch = _torch()
+    import torch.autograd.forward_ad as fwd
+    x, y = torch.randn(3, 64, device="cuda"), torch.randn(3, 64, device="cuda")
+    w, s = torch.full((8, 32), 0x99, dtype=torch.uint8, device="cuda"), torch.ones(8, 1, dtype=torch.float16, device="cuda")
+    with fwd.dual_level():
+        dual = fwd.make_dual(x, torch.ones_like(x))
+        for call in (lambda: gam.gam_residual_norm(dual, y), lambda: gam.gam_residual_norm(x, dual),
+                     lambda: gam.gam_quant_linear(dual, w, s)):
+            with pytest.raises(gam.GamError, match="gradient"):
+                call()
+        gam.gam_residual_norm(fwd.unpack_dual(dual).primal.detach(), y)
