@@ -98,6 +98,8 @@ struct Call {
     if (packed ? !t.is_contiguous() : shape.back() > 1 && t.stride(-1) != 1)
       refuse(GAM_ERR_INVALID_ARG, packed ? std::string(name) + " must be contiguous"
                                          : std::string("the last dimension of ") + name + " must be contiguous");
+    if (t.is_neg())  // its memory holds the negated values
+      refuse(GAM_ERR_INVALID_ARG, std::string(name) + " is a lazily negated view: call it with resolve_neg()");
     return t.data_ptr();
   }
 

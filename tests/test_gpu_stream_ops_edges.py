@@ -254,3 +254,16 @@ def test_forward_mode_tangents_are_refused():
             with pytest.raises(gam.GamError, match="gradient"):
                 call()
         gam.gam_residual_norm(fwd.unpack_dual(dual).primal.detach(), y)
+
+
+def test_lazily_negated_views_are_refused():
+    """Such a tensor's memory holds the negated values."""
+    torch = _torch()
+    z = torch.randn(6, 1, dtype=torch.complex64, device="cuda")
+    x = z.conj().imag
+    assert x.is_neg()
+    with pytest.raises(gam.GamError) as e:
+        gam.gam_residual_norm(x, torch.zeros(6, 1, device="cuda"))
+    assert e.value.name == "GAM_ERR_INVALID_ARG"
+    xo, _ = gam.gam_residual_norm(x.resolve_neg(), torch.zeros(6, 1, device="cuda"))
+    assert torch.equal(xo, x)
