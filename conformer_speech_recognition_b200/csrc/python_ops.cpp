@@ -14,6 +14,7 @@
 #include <c10/core/AutogradState.h>
 #include <ATen/ops/empty.h>
 
+#include <initializer_list>
 #include <optional>
 #include <string>
 
@@ -109,8 +110,14 @@ struct Call {
     return THPVariable_Wrap(at::empty(shape, at::TensorOptions().dtype(type).device(c10::kCUDA, dev)));
   }
 
-  void check(gam_status s) const {
+  // The status of a call that writes these tensors: what was given counts as changed in place (autograd then notices
+  // if a backward pass has saved it).
+  void check(gam_status s, std::initializer_list<PyObject*> written) const {
     if (s != GAM_OK) refuse(s, g_entry.last_error(nullptr));
+    for (PyObject* o : written) {
+      const at::Tensor& t = THPVariable_Unpack(o);
+      if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+    }
   }
 };
 
@@ -178,7 +185,7 @@ PyObject* quant_linear(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
         (const uint8_t*)call.arg(a[1], "packed", {n, k / 2}, at::kByte, true),
         call.arg(a[2], "scale", {n, k / 64}, at::kHalf, true),
         (const float*)call.arg(a[3], "bias", {n}, at::kFloat, true, true), code(a[4]), (int)rows, (int)n, (int)k, y,
-        THPVariable_Unpack(out.p).stride(0), call.raw));
+        THPVariable_Unpack(out.p).stride(0), call.raw), {out.p});
     return out.release();
   });
 }
@@ -203,7 +210,7 @@ PyObject* short_conv(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
         (const float*)call.arg(a[1], "weight", {d, taps}, at::kFloat, true),
         (const float*)call.arg(a[2], "bias", {d}, at::kFloat, true, true), (int)taps, code(a[3]), (int)B, (int)t, (int)d,
         (const int32_t*)call.arg(a[4], "lengths", {B}, at::kInt, true, true),
-        call.arg(a[5], "state", {B, taps - 1, d}, type, true, true), so, y, ot.stride(0), ot.stride(1), call.raw));
+        call.arg(a[5], "state", {B, taps - 1, d}, type, true, true), so, y, ot.stride(0), ot.stride(1), call.raw), {out.p, state.p});
     return pair_of(out, state);
   });
 }
@@ -240,7 +247,7 @@ PyObject* selective_scan(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
     p.lengths = (const int32_t*)call.arg(a[9], "lengths", {B}, at::kInt, true, true);
     p.state_in = (const float*)call.arg(a[10], "state", {B, d, n}, at::kFloat, true, true);
     p.batch = (int)B, p.t_max = (int)t, p.d = (int)d, p.n = (int)n;
-    call.check(g_entry.selective_scan(&p, call.raw));
+    call.check(g_entry.selective_scan(&p, call.raw), {out.p, state.p});
     return pair_of(out, state);
   });
 }
@@ -290,7 +297,7 @@ PyObject* residual_norm(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
     p.eps = (float)PyFloat_AsDouble(a[12]);
     if (PyErr_Occurred()) throw PyErr_Occurred();
     p.rows = rows, p.d = (int)d;
-    call.check(g_entry.residual_norm(&p, call.raw));
+    call.check(g_entry.residual_norm(&p, call.raw), {x_out.p, out.p});
     return pair_of(x_out, out);
   });
 }

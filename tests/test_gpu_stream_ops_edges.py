@@ -267,3 +267,23 @@ def test_lazily_negated_views_are_refused():
     assert e.value.name == "GAM_ERR_INVALID_ARG"
     xo, _ = gam.gam_residual_norm(x.resolve_neg(), torch.zeros(6, 1, device="cuda"))
     assert torch.equal(xo, x)
+
+
+def test_outputs_count_as_changed():
+    """A tensor that a call writes counts one change, so that a backward pass which saved it notices."""
+    torch = _torch()
+    w = torch.ones(4, 32, device="cuda", requires_grad=True)
+    x, y = torch.randn(4, 32, device="cuda"), torch.randn(4, 32, device="cuda")
+    loss = (w * x).sum()                               # saves x
+    with torch.no_grad():
+        gam.gam_residual_norm(x, y, x_out=x)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        loss.backward()
+    v = torch.randn(2, 3, 8, device="cuda")
+    out, st = torch.empty_like(v), torch.zeros(2, 3, 8, device="cuda")
+    before = out._version, st._version, v._version
+    gam.gam_short_conv(v, torch.ones(8, 4, device="cuda"), state=st, out=out, state_out=st)
+    assert (out._version, st._version, v._version) == (before[0] + 1, before[1] + 1, before[2])
+    with torch.inference_mode():                       # these keep no count
+        a = torch.randn(4, 32, device="cuda")
+        gam.gam_residual_norm(a, torch.randn(4, 32, device="cuda"), x_out=a)
