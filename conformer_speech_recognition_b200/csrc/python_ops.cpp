@@ -243,7 +243,8 @@ PyObject* selective_scan(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
     p.d_skip = (const float*)call.arg(a[5], "d_skip", {d}, at::kFloat, true, true);
     p.z = strided(a[6], "z", d, p.z_batch_stride, p.z_row_stride, true);
     p.dt_bias = (const float*)call.arg(a[7], "dt_bias", {d}, at::kFloat, true, true);
-    p.dt_softplus = PyObject_IsTrue(a[8]) == 1;
+    p.dt_softplus = PyObject_IsTrue(a[8]);
+    if (p.dt_softplus < 0) throw PyErr_Occurred();
     p.lengths = (const int32_t*)call.arg(a[9], "lengths", {B}, at::kInt, true, true);
     p.state_in = (const float*)call.arg(a[10], "state", {B, d, n}, at::kFloat, true, true);
     p.batch = (int)B, p.t_max = (int)t, p.d = (int)d, p.n = (int)n;

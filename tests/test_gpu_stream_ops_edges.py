@@ -287,3 +287,11 @@ def test_outputs_count_as_changed():
     with torch.inference_mode():                       # these keep no count
         a = torch.randn(4, 32, device="cuda")
         gam.gam_residual_norm(a, torch.randn(4, 32, device="cuda"), x_out=a)
+
+
+def test_scan_softplus_flag_without_a_truth_value():
+    torch = _torch()
+    t, _ = scan_inputs(38, 1, 2, 8, 4, "f32")
+    with pytest.raises(ValueError):
+        scan_call(t, dt_softplus=np.array([True, False]))
+    torch.cuda.synchronize()
