@@ -4,8 +4,10 @@ Compiles every ``csrc/*.cu`` for sm_100a with nvcc (object files under
 ``_build/`` at the repository root, in parallel) and links them into
 ``conformer_speech_recognition_b200/libgam.so``.  nvcc cross-compiles, so this
 runs on a machine without a GPU.  ``csrc/python_ops.cpp`` (the marshalling of
-the streaming-block operators' Python calls) is compiled against torch's headers
-into ``conformer_speech_recognition_b200/_ops.so`` beside it.
+the streaming-block operators' Python calls) is compiled with g++ against torch's
+headers into ``conformer_speech_recognition_b200/_ops.so`` beside it.  The library
+itself needs nvcc alone: without torch the module is left out, and an error of its
+compilation is raised after the library is there.
 
     python -m conformer_speech_recognition_b200.build [--force] [-j N]
 """
@@ -65,7 +67,11 @@ def _build_ops(force: bool) -> None:
     newest = max(os.path.getmtime(src), os.path.getmtime(os.path.join(ROOT, "include", "gam.h")))
     if not force and os.path.exists(OPS) and os.path.getmtime(OPS) >= newest:
         return
-    torch = importlib.util.find_spec("torch").submodule_search_locations[0]
+    spec = importlib.util.find_spec("torch")
+    if spec is None:
+        print("torch is not installed: _ops.so, which its Python calls need, is not built", file=sys.stderr)
+        return
+    torch = spec.submodule_search_locations[0]
     inc, lib = os.path.join(torch, "include"), os.path.join(torch, "lib")
     cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
     cmd = [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
@@ -85,13 +91,13 @@ def build(force: bool = False, jobs: int = 8, verbose: bool = False, extra=()) -
     with cf.ThreadPoolExecutor(max_workers=jobs) as ex:
         ops = ex.submit(_build_ops, force)
         objs = list(ex.map(lambda s: _compile(s, force, hdr, list(extra)), srcs))
-        ops.result()
     newest = max(os.path.getmtime(o) for o in objs)
     if force or not os.path.exists(LIB) or os.path.getmtime(LIB) < newest:
         cmd = [nvcc(), *ARCH, "-shared", "-o", LIB, *objs, "-lcudart"]
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
             raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
+    ops.result()
     if verbose:
         print(LIB)
     return LIB
