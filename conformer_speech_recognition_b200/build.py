@@ -15,6 +15,7 @@ from __future__ import annotations
 
 import argparse
 import concurrent.futures as cf
+import importlib.metadata
 import importlib.util
 import os
 import shutil
@@ -28,6 +29,7 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libgam.so")
 OPS = os.path.join(PKG, "_ops.so")
+OPS_MARK = "gam _ops built for "
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
@@ -62,20 +64,36 @@ def _compile(src: str, force: bool, hdr_mtime: float, extra) -> str:
     return obj
 
 
+def _torch_version() -> str:
+    try:
+        return importlib.metadata.version("torch")
+    except importlib.metadata.PackageNotFoundError:  # a torch on the path that was not installed
+        return "of unknown version"
+
+
+def _built_for(path: str) -> bytes:
+    """What a module was compiled against, from the mark that it holds (b"" if there is none)."""
+    if not os.path.exists(path):
+        return b""
+    with open(path, "rb") as f:
+        return f.read().partition(OPS_MARK.encode())[2].partition(b";")[0]
+
+
 def _build_ops(force: bool) -> None:
     src = os.path.join(CSRC, "python_ops.cpp")
     newest = max(os.path.getmtime(src), os.path.getmtime(os.path.join(ROOT, "include", "gam.h")))
-    if not force and os.path.exists(OPS) and os.path.getmtime(OPS) >= newest:
-        return
     spec = importlib.util.find_spec("torch")
     if spec is None:
         print("torch is not installed: _ops.so, which its Python calls need, is not built", file=sys.stderr)
+        return
+    against = f"torch {_torch_version()} {sys.implementation.cache_tag}"
+    if not force and os.path.exists(OPS) and os.path.getmtime(OPS) >= newest and _built_for(OPS) == against.encode():
         return
     torch = spec.submodule_search_locations[0]
     inc, lib = os.path.join(torch, "include"), os.path.join(torch, "lib")
     cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
     cmd = [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
-           "-I", inc, "-I", os.path.join(inc, "torch", "csrc", "api", "include"),
+           f'-DGAM_BUILT_FOR="{OPS_MARK}{against};"', "-I", inc, "-I", os.path.join(inc, "torch", "csrc", "api", "include"),
            "-I", sysconfig.get_paths()["include"], "-isystem", os.path.join(cuda, "include"), src, "-o", OPS + ".tmp",
            "-L", lib, "-Wl,-rpath," + lib, "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10_cuda", "-lc10"]
     r = subprocess.run(cmd, capture_output=True, text=True)

@@ -329,4 +329,9 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_ops", "Marshalling of the streami
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__ops() { return PyModule_Create(&module); }
+// The attribute built_for also leaves its text in the file, where the build looks for it.
+PyMODINIT_FUNC PyInit__ops() {
+  PyObject* m = PyModule_Create(&module);
+  if (m && PyModule_AddStringConstant(m, "built_for", GAM_BUILT_FOR) < 0) Py_CLEAR(m);
+  return m;
+}
