@@ -295,3 +295,105 @@ def test_scan_softplus_flag_without_a_truth_value():
     with pytest.raises(ValueError):
         scan_call(t, dt_softplus=np.array([True, False]))
     torch.cuda.synchronize()
+
+
+# ---- the forms of large calls ---------------------------------------------------------
+
+@pytest.mark.parametrize("xdtype,dtype", [("f32", "f32"), ("f32", "f16"), ("bf16", "bf16")])
+@pytest.mark.parametrize("d,extra,per,gate_act", [
+    (64, 0, 1, "swish"), (256, 0, 0, "none"), (512, 0, 7, "tanh"), (500, 0, 1, "sigmoid"), (1000, 0, 0, "none"), (1024, 0, 1, "swish"),
+    (62, 0, 1, "sigmoid"), (201, 0, 1, "swish"), (250, 0, 5000, "none"), (201, 2, 0, "none"), (257, 0, 1, "tanh"), (61, 1, 7, "swish"),
+    (1024, 8, 1, "sigmoid"), (1040, 0, 0, "none")])
+def test_norm_many_rows(xdtype, dtype, d, extra, per, gate_act):
+    """Rows enough for warps to walk over several of them: aligned rows, odd ones, rows further apart than d; in place too."""
+    torch = _torch()
+    rng = np.random.default_rng(d + extra)
+    rows = 4998 if per == 7 else 5000
+
+    def make(name, std):
+        base = torch.full((rows, d + extra), float("nan"), dtype=_dt(name), device="cuda")
+        base[:, :d] = dev((rng.normal(size=(rows, d)) * std).astype(np.float32))
+        return base, base[:, :d]
+    (bx, x), (by, y) = make(xdtype, 2.0), make(dtype, 1.0)
+    kt = {k: dev(rng.normal(size=d).astype(np.float32)) for k in ("post_weight", "post_bias", "pre_weight", "pre_bias", "layer_scale")}
+    if per:
+        kt["gate"] = dev(rng.normal(size=(rows // per, d)).astype(np.float32), _dt(dtype))
+    kw = dict(post="layer", pre="layer", gate_act=gate_act, alpha=0.5)
+    xf, yf = x.clone(), y.clone()
+    xo, u = gam.gam_residual_norm(x, y, **kw, **kt)
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    # the first and last rows, some between, and where warps come to their second row
+    pick = np.unique(np.r_[0:6, rng.integers(0, rows, 16), [v for v in (k * sms * 4 + i for k in (3, 5, 8) for i in (-1, 0, 1)) if v < rows], rows - 6:rows])
+    some = dev(pick.astype(np.int64))
+    ref = dict(kw, **{k: host(v) for k, v in kt.items() if k != "gate"})
+    if per:
+        ref["gate"] = host(kt["gate"].index_select(0, some // per))
+    norm_check(xo.index_select(0, some), u.index_select(0, some), host(xf.index_select(0, some)), host(yf.index_select(0, some)),
+               xdtype, dtype, ref)
+    gam.gam_residual_norm(x, y, x_out=x, out=y, **kw, **kt)
+    assert torch.equal(x, xo) and torch.equal(y, u)
+    if extra:
+        assert bool(torch.isnan(bx[:, d:]).all()) and bool(torch.isnan(by[:, d:]).all())
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("B,T,d,n,z", [
+    (64, 40, 1272, 7, True), (64, 40, 1273, 8, False), (64, 50, 640, 16, True), (64, 45, 601, 11, True), (40, 70, 512, 32, False),
+    (40, 66, 497, 30, True), (40, 70, 256, 64, True), (40, 67, 243, 50, False)])
+def test_scan_many_channels(dtype, B, T, d, n, z):
+    """Two channels to a lane, over four tiles of frames and more; ragged."""
+    torch = _torch()
+    t, f = scan_inputs(B + T + d + n, B, T, d, n, dtype, z=z)
+    lens = [T - (i * 5) % (T + 1) for i in range(B)]
+    lens[1], lens[2] = 0, 1
+    for i, m in enumerate(lens):
+        for name in ("x", "dt", "b", "c") + (("z",) if z else ()):
+            t[name][i, m:] = float("nan")
+    ln = dev(np.array(lens, np.int32))
+    y, new = scan_call(t, ln)
+    some = [0, 1, 2, 7, B - 1]
+    pick = dev(np.array(some, np.int64))
+    part = {k: (None if v is None else v[some] if k in ("x", "dt", "b", "c", "z", "state") else v) for k, v in f.items()}
+    scan_check(y.index_select(0, pick), new.index_select(0, pick), part, [lens[i] for i in some], dtype)
+    # the other sequences: as in a call of their own, which another form serves
+    for i in (3, B // 2):
+        one = {k: (v if v is None or k in ("a", "d_skip", "dt_bias") else v[i:i + 1]) for k, v in t.items()}
+        y1, s1 = scan_call(one, ln[i:i + 1])
+        alone = {k: (None if v is None else v[i:i + 1] if k in ("x", "dt", "b", "c", "z", "state") else v) for k, v in f.items()}
+        scan_check(y1, s1, alone, [lens[i]], dtype)
+        scan_check(y[i:i + 1], new[i:i + 1], alone, [lens[i]], dtype)
+    y2, s2 = scan_call(t, ln, state_out=t["state"])
+    assert torch.equal(y2, y) and torch.equal(s2, new)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("B,T,d,taps", [(32, 90, 2048, 2), (32, 95, 2048, 3), (32, 90, 2048, 5), (32, 97, 2048, 7), (32, 90, 2048, 8),
+                                        (40, 21, 2047, 4), (40, 30, 2047, 6)])
+def test_conv_many_rows(dtype, B, T, d, taps):
+    """Eight rows of a segment on their way at a time; ragged."""
+    torch = _torch()
+    rng = np.random.default_rng(T + d + taps)
+    x, xf = normal(rng, B, T, d, dtype=dtype)
+    s, sf = normal(rng, B, taps - 1, d, dtype=dtype)
+    w, b = rng.normal(size=(d, taps)).astype(np.float32), rng.normal(size=d).astype(np.float32)
+    lens = [T - (i * 7) % (T + 1) for i in range(B)]
+    lens[1], lens[2] = 0, 1
+    for i, m in enumerate(lens):
+        x[i, m:] = float("nan")
+    y, new = gam.gam_short_conv(x, dev(w), bias=dev(b), act="swish", lengths=dev(np.array(lens, np.int32)), state=s)
+    some = [0, 1, 2, 9, B - 1]
+    pick = dev(np.array(some, np.int64))
+    conv_check(y.index_select(0, pick), new.index_select(0, pick), xf[some], w, b, [lens[i] for i in some], sf[some], "swish", dtype,
+               True)
+    for i in (3, B // 2, B - 2):                       # the other forms give the same bits
+        y1, s1 = gam.gam_short_conv(x[i:i + 1], dev(w), bias=dev(b), act="swish", lengths=dev(np.array(lens[i:i + 1], np.int32)),
+                                    state=s[i:i + 1])
+        assert torch.equal(y1[0], y[i]) and torch.equal(s1[0], new[i])
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("rows", [24, 40, 64])
+def test_linear_many_rows_and_weights(dtype, rows):
+    x, xf, q, scale, b = linear_inputs(rows, rows, 4101, 2112, dtype, True)
+    y = gam.gam_quant_linear(x, dev(gam.gam_quant_linear_pack(q)), dev(scale), bias=dev(b), act="swish")
+    linear_check(y, xf, q, scale, b, "swish", dtype)
