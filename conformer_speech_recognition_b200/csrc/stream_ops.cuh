@@ -145,10 +145,10 @@ __device__ __forceinline__ float rcp_approx(float v) {
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
   return r;
 }
-// v between lo and hi; NaN stays.
-__device__ __forceinline__ float clamp_f(float v, float lo, float hi) {
+// v between -bound and bound; NaN stays.  A negative bound gives the negated value.
+__device__ __forceinline__ float bound_f(float v, float bound) {
   float r;
-  asm("{\n\t.reg .f32 t;\n\tmax.NaN.f32 t, %1, %2;\n\tmin.NaN.f32 %0, t, %3;\n\t}" : "=f"(r) : "f"(v), "f"(lo), "f"(hi));
+  asm("min.NaN.xorsign.abs.f32 %0, %1, %2;" : "=f"(r) : "f"(v), "f"(bound));
   return r;
 }
 
@@ -165,7 +165,7 @@ __device__ __forceinline__ u64 exp2v(u64 v) {
 // reciprocal.  Below -87 the reciprocal is 0, at most 2e-38 off.
 __device__ __forceinline__ u64 sigmoid2(u64 v) {
   const float2 w = unpack2(v);
-  const u64 e = exp2v(pack2(clamp_f(-w.x, -200.f, 200.f), clamp_f(-w.y, -200.f, 200.f)));
+  const u64 e = exp2v(pack2(bound_f(w.x, -200.f), bound_f(w.y, -200.f)));
   const float2 q = unpack2(fma2(e, both(1.f), both(1.f)));
   return pack2(rcp_approx(q.x), rcp_approx(q.y));
 }
