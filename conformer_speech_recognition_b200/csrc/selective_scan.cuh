@@ -649,8 +649,12 @@ __global__ void __launch_bounds__(kStep) step_kernel(const gam_scan_args p) {
   const int part = threadIdx.x % L, c0 = cb * CT * CH + threadIdx.x / L;
   const int k0 = part * 4;
   const int len = length_of(p, b);
-  float a[CH][4], h[CH][4], skip[CH], bias[CH];
-  int ch[CH];
+  // the channels whose outputs a lane finishes: of L lanes the even ones take the first, the odd ones the second
+  constexpr int OWN = L > 1 ? 1 : CH;
+  const bool up = part & 1;
+  float a[CH][4], h[CH][4], bias[CH], skip[OWN];
+  int ch[CH], own[OWN];
+  bool live[OWN];
 #pragma unroll
   for (int j = 0; j < CH; ++j) {
     ch[j] = min(c0 + j * CT, p.d - 1);               // lanes past the last channel walk along, for the shuffles
@@ -675,8 +679,13 @@ __global__ void __launch_bounds__(kStep) step_kernel(const gam_scan_args p) {
           a[j][i] = __ldg(pa + i);
         }
     }
-    skip[j] = p.d_skip ? __ldg(p.d_skip + ch[j]) : 0.f;
     bias[j] = p.dt_bias ? __ldg(p.dt_bias + ch[j]) : 0.f;
+  }
+#pragma unroll
+  for (int j = 0; j < OWN; ++j) {
+    own[j] = L > 1 && up ? ch[CH - 1] : ch[j];
+    live[j] = part < 2 && c0 + (L > 1 ? part : j) * CT < p.d;
+    skip[j] = p.d_skip ? __ldg(p.d_skip + own[j]) : 0.f;
   }
   const T* px = (const T*)p.x + b * p.x_batch_stride;
   const T* pdt = (const T*)p.dt + b * p.dt_batch_stride;
@@ -685,13 +694,14 @@ __global__ void __launch_bounds__(kStep) step_kernel(const gam_scan_args p) {
   const T* pc = (const T*)p.c + b * p.c_batch_stride + k0;
   T* y = (T*)p.y + b * p.y_batch_stride;
   for (int t = 0; t < len; ++t) {
-    uint32_t ux[CH], ud[CH], uz[CH], ub[4], uc[4];
+    uint32_t ux[CH], ud[CH], uz[OWN], ub[4], uc[4];
 #pragma unroll
     for (int j = 0; j < CH; ++j) {
       ud[j] = load_bits(pdt + t * p.dt_row_stride + ch[j]);
       ux[j] = load_bits(px + t * p.x_row_stride + ch[j]);
-      uz[j] = pz ? load_bits(pz + t * p.z_row_stride + ch[j]) : 0;
     }
+#pragma unroll
+    for (int j = 0; j < OWN; ++j) uz[j] = pz ? load_bits(pz + t * p.z_row_stride + own[j]) : 0;
     float bv[4] = {}, cv[4] = {};
     if constexpr (QUAD) {                            // rows of b and c in whole quads, n a multiple of 4
       if (k0 < p.n) {
@@ -714,10 +724,12 @@ __global__ void __launch_bounds__(kStep) step_kernel(const gam_scan_args p) {
     }
     float2 s = make_float2(from_bits<T>(ud[0]) + bias[0], from_bits<T>(ud[1]) + bias[1]);
     if (p.dt_softplus) s = softplus2(s);
+    float v[CH], xv[CH];
 #pragma unroll
     for (int j = 0; j < CH; ++j) {
-      const float st = j ? s.y : s.x, xv = from_bits<T>(ux[j]), sx = st * xv, e = st * kLog2e;
-      float v = 0.f;
+      xv[j] = from_bits<T>(ux[j]);
+      const float st = j ? s.y : s.x, sx = st * xv[j], e = st * kLog2e;
+      v[j] = 0.f;
 #pragma unroll
       for (int i = 0; i < 4; i += 2) {
         // the rates are bounded here, not where they are loaded: the loads of the frame would wait for them (+0.5 us)
@@ -728,23 +740,32 @@ __global__ void __launch_bounds__(kStep) step_kernel(const gam_scan_args p) {
           if (k0 + i >= p.n) h[j][i] = 0.f;
           if (k0 + i + 1 >= p.n) h[j][i + 1] = 0.f;
         }
-        v = fmaf(cv[i], h[j][i], v);
-        v = fmaf(cv[i + 1], h[j][i + 1], v);
+        v[j] = fmaf(cv[i], h[j][i], v[j]);
+        v[j] = fmaf(cv[i + 1], h[j][i + 1], v[j]);
       }
-      if (VEC && k0 >= p.n) v = 0.f;
+      if (VEC && k0 >= p.n) v[j] = 0.f;
+    }
+    if constexpr (L > 1) {
+      v[0] = (up ? v[1] : v[0]) + __shfl_xor_sync(0xffffffffu, up ? v[0] : v[1], 1);
 #pragma unroll
-      for (int o = L / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-      v = fmaf(skip[j], xv, v);
-      if (pz) v *= swish_f<T>(from_bits<T>(uz[j]));
-      if (c0 + j * CT < p.d && part == 0) y[t * p.y_row_stride + ch[j]] = from_f<T>(v);
+      for (int o = 2; o < L; o <<= 1) v[0] += __shfl_xor_sync(0xffffffffu, v[0], o);
+      xv[0] = up ? xv[1] : xv[0];
+    }
+#pragma unroll
+    for (int j = 0; j < OWN; ++j) {
+      float q = fmaf(skip[j], xv[j], v[j]);
+      if (pz) q *= swish_f<T>(from_bits<T>(uz[j]));
+      if (live[j]) y[t * p.y_row_stride + own[j]] = from_f<T>(q);
     }
   }
 #pragma unroll
+  for (int j = 0; j < OWN; ++j)
+    if (live[j])
+      for (int t = len; t < p.t_max; ++t) y[t * p.y_row_stride + own[j]] = from_f<T>(0.f);
+  if (!p.state_out) return;
+#pragma unroll
   for (int j = 0; j < CH; ++j) {
     if (c0 + j * CT >= p.d) continue;
-    if (part == 0)
-      for (int t = len; t < p.t_max; ++t) y[t * p.y_row_stride + ch[j]] = from_f<T>(0.f);
-    if (!p.state_out) continue;
     float* ph = p.state_out + ((int64_t)b * p.d + ch[j]) * p.n + k0;
     if constexpr (VEC) {
       if (k0 < p.n) *reinterpret_cast<float4*>(ph) = make_float4(h[j][0], h[j][1], h[j][2], h[j][3]);
