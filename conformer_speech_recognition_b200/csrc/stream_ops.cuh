@@ -176,7 +176,11 @@ __device__ __forceinline__ u64 swish2(u64 v) { return mul2(v, sigmoid2(v)); }
 // more.
 template <typename T>
 __device__ __forceinline__ float sigmoid_f(float v) {
-  if constexpr (std::is_same_v<T, float>) return unpack2(sigmoid2(both(v))).x;
+  if constexpr (std::is_same_v<T, float>) {  // as sigmoid2
+    const float w = bound_f(v, -200.f), t = w * 1.4426950408889634f;
+    const float d = fmaf(t, 1.9046543e-9f, fmaf(t, -0.69314718246459961f, w));
+    return rcp_approx(1.f + exp2_approx(t) * (1.f + d));
+  }
   return rcp_approx(1.f + exp2_approx(v * -1.4426950408889634f));
 }
 template <typename T>
