@@ -72,6 +72,25 @@ struct Call {
     }
   }
 
+  // A tensor's gradient, which these operators do not give, is not dropped in silence.
+  static void no_gradient(const at::Tensor& t, const char* name) {
+    // a forward-mode tangent does not make a tensor require a gradient, and no_grad does not switch it off
+    if (c10::AutogradState::get_tls_state().get_fw_grad_mode() && t._fw_grad(0).defined())
+      refuse(GAM_ERR_INVALID_ARG, std::string(name) + " carries a forward-mode gradient, which this operator does not "
+                                                      "pass on: call it with detached tensors");
+    if (t.requires_grad() && at::GradMode::is_enabled())
+      refuse(GAM_ERR_INVALID_ARG, std::string(name) + " requires a gradient, which this operator does not give: call it "
+                                                      "under torch.no_grad() or with detached tensors");
+  }
+
+  // A number, or a tensor that holds one.
+  static float number(PyObject* o, const char* name) {
+    if (THPVariable_Check(o)) no_gradient(THPVariable_Unpack(o), name);
+    const double v = PyFloat_AsDouble(o);
+    if (PyErr_Occurred()) throw PyErr_Occurred();
+    return (float)v;
+  }
+
   // Address of a tensor of this shape and type on the call's device; its last dimension
   // is contiguous (`packed`: all of it).  None is 0 where `optional`.
   void* arg(PyObject* o, const char* name, at::IntArrayRef shape, at::ScalarType type, bool packed,
@@ -89,13 +108,7 @@ struct Call {
       for (int64_t v : shape) want += (want.empty() ? "" : ", ") + std::to_string(v);
       refuse(GAM_ERR_INVALID_ARG, std::string(name) + " must have shape [" + want + "]");
     }
-    // a forward-mode tangent does not make a tensor require a gradient, and no_grad does not switch it off
-    if (c10::AutogradState::get_tls_state().get_fw_grad_mode() && t._fw_grad(0).defined())
-      refuse(GAM_ERR_INVALID_ARG, std::string(name) + " carries a forward-mode gradient, which this operator does not "
-                                                      "pass on: call it with detached tensors");
-    if (t.requires_grad() && at::GradMode::is_enabled())
-      refuse(GAM_ERR_INVALID_ARG, std::string(name) + " requires a gradient, which this operator does not give: call it "
-                                                      "under torch.no_grad() or with detached tensors");
+    no_gradient(t, name);
     if (packed ? !t.is_contiguous() : shape.back() > 1 && t.stride(-1) != 1)
       refuse(GAM_ERR_INVALID_ARG, packed ? std::string(name) + " must be contiguous"
                                          : std::string("the last dimension of ") + name + " must be contiguous");
@@ -278,7 +291,7 @@ PyObject* residual_norm(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
     p.y = row(a[1], "y", yt, p.y_stride);
     p.x_out = row(x_out.p, "x_out", xt, p.x_out_stride);
     p.u = row(out.p, "out", yt, p.u_stride);
-    p.alpha = (float)PyFloat_AsDouble(a[2]);
+    p.alpha = call.number(a[2], "alpha");
     p.layer_scale = vec(a[3], "layer_scale");
     p.gate_rows = 1;
     if (a[4] != Py_None) {
@@ -295,8 +308,7 @@ PyObject* residual_norm(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
     p.pre_norm = code(a[9]);
     p.pre_weight = vec(a[10], "pre_weight");
     p.pre_bias = vec(a[11], "pre_bias");
-    p.eps = (float)PyFloat_AsDouble(a[12]);
-    if (PyErr_Occurred()) throw PyErr_Occurred();
+    p.eps = call.number(a[12], "eps");
     p.rows = rows, p.d = (int)d;
     call.check(g_entry.residual_norm(&p, call.raw), {x_out.p, out.p});
     return pair_of(x_out, out);

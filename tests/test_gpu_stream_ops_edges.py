@@ -297,6 +297,20 @@ def test_scan_softplus_flag_without_a_truth_value():
     torch.cuda.synchronize()
 
 
+def test_norm_scale_that_requires_a_gradient_is_refused():
+    torch = _torch()
+    x, y = torch.randn(3, 32, device="cuda"), torch.randn(3, 32, device="cuda")
+    alpha = torch.tensor(0.5, device="cuda", requires_grad=True)
+    with pytest.raises(gam.GamError, match="alpha requires a gradient"):
+        gam.gam_residual_norm(x, y, alpha=alpha)
+    want = gam.gam_residual_norm(x, y, alpha=0.5)
+    with torch.no_grad():
+        got = gam.gam_residual_norm(x, y, alpha=alpha)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    with pytest.raises(TypeError):
+        gam.gam_residual_norm(x, y, alpha="half")
+
+
 # ---- the forms of large calls ---------------------------------------------------------
 
 @pytest.mark.parametrize("xdtype,dtype", [("f32", "f32"), ("f32", "f16"), ("bf16", "bf16")])
