@@ -2,24 +2,30 @@
 //
 //   y[m, o] = act(bias[o] + sum_g scale[o, g] sum_{j in g} q[o, j] x[m, j])
 //
-// The weights are read once and the rows are few, so the bound is the weight
-// stream (0.53 bytes per weight) and, close behind it, the instructions that turn
-// integers into an MMA operand.  A warp owns 16 outputs: mma.m16n8k16 with the
-// weights as the 16-row operand and rows of x as 8-column tiles (the operand stays in
-// registers: at most 64 rows there is too little reuse to pay for the shared-memory tiles
-// and tensor memory that tcgen05 works on).  The integers are exact in both 16-bit
-// types, so a group's sum is that of q x itself and is scaled in fp32 by the group's scale.
+// The floor is the weight stream (0.53 bytes per weight).  A warp owns 16 outputs:
+// mma.m16n8k16 with the weights as the 16-row operand, dequantised in registers, and
+// rows of x as 8-column tiles.  The integers are exact in both 16-bit types, so a
+// group's sum is that of q x itself and is scaled in fp32 by the group's scale.
+// Weights are read and dequantised once for every 8 rows (one tile of x) or 16 (two):
+// once for up to 16 rows, four times for 64, and in fp32 once for every 8 rows above 16.
+// (tcgen05 would take 128 outputs and all rows at once, with an accumulator of its own
+// for every group's scale; not built.)
 //
-// What it measured: one row of 768 x 768 in 2.4 us (launch and one trip to memory); one row of
-// 16384 x 4096 in 14 us (36 MB of weights, 2.6 TB/s) and 16 rows in 19.5 us: 8.0 M instructions at
-// 1.7 a clock, 16 warps to an SM by their registers, lines in the L1 77 % of the time.
+// What it measured: one row of 768 x 768 in 2.4 us (launch and one trip to memory); 16384 x 4096
+// (36 MB of weights, 5.4 us at the copy rate): one row in 13.6 us, 16 in 19.6, 32 in 36, 64 in 62; in
+// fp32 16 in 40, 32 in 128, 64 in 252.  No pipe bounds them (16 rows: 1.7 of 4 instructions a clock, ALU 38 %): it
+// is the latency at 16 warps to an SM, as many as their registers allow, and the uneven last
+// round of CTAs (512 at two to an SM; up to 8 rows 256, of which 108 SMs hold two and 40 one).
 //
-// The words' nibble order gives adjacent pairs by one shift and mask, and a lane's 16
+// Integers become floats through the mantissa of 1024 (fp16) or 128 (bf16), a published
+// method.  The words' nibble order gives adjacent pairs by one shift and mask, and a lane's 16
 // weights of a group are 16 consecutive k, so its fragments of x are 16 consecutive
 // values of a row.  K is split over the warps of a CTA, and over a cluster of CTAs when
 // there are few tiles; partial sums are added in a fixed order.
 //
-// fp32 x is held as three bf16 parts (8 + 8 + 8 bits: exact), each with its own MMA.
+// fp32 x is held as three bf16 parts (8 + 8 + 8 bits: exact), each with its own MMA, whose
+// fp32 sums within a group may truncate (2 u an addition; 1025 outputs of 1024 in all 2.8e-7
+// off, an fp32 sum 1.8e-7).
 #include <cooperative_groups.h>
 
 #include <algorithm>

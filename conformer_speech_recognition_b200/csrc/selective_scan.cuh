@@ -19,8 +19,8 @@
 // thread does both, with two channels to a lane (32 x 390 frames of 2048 channels: 179 us,
 // with producers 249), which halves the reads of b and c.
 //
-// What it measured (16 states): 12.5 k frames of 2048 channels in 209 us, the special-function
-// pipe 57 % busy (exponentials and the gates' reciprocals) and 1.8 instructions a clock; the main loop alone, without
+// What it measured (16 states): 12.5 k frames of 2048 channels in 210 us, the special-function
+// pipe 56 % busy (exponentials and the gates' reciprocals) and 1.9 instructions a clock; the main loop alone, without
 // the producers' work, runs at 91 % of that pipe's rate.  A share of the exponentials as polynomials on the
 // fp32 pipe was slower (one pair in 4: +5 %): the instructions it adds cost more than the
 // pipe it frees.
@@ -31,6 +31,10 @@
 // of a channel's decays is exp(a sum s)), the pieces are joined in frame order
 // over distributed shared memory, and each CTA runs its piece again from its true
 // state.  Twice the exponentials, R times the SMs.
+//
+// A tile runs all its frames whatever is valid (32 with 16 states on small calls, 8 on large
+// ones), so that 5 frames take the time of a tile: one stream of 2048 channels 3.6 us for 4
+// frames, 4.6 for 5 to 32; 64 streams 10.5 for 4, 15.3 for 5 to 8, 34 for 32.
 //
 // Few frames (step_kernel, t_max <= 4): the states are the traffic; a thread holds
 // 4 states of two channels (16-byte accesses) and keeps them in registers over the frames.
@@ -82,7 +86,7 @@ __device__ __forceinline__ u64 exp2_poly2(u64 x) {
 // 2^x (2^-22) an fp32 call's outputs came out 1e-6 off, so fp32 calls take the polynomial.  16-bit calls keep the
 // hardware's, but not its mean error: that is -6e-9 for x in -0.003 .. 0 and -2e-8 in -0.7 .. -0.003 (measured),
 // so x is raised by kRaise, which the multiply-add gives for nothing and which leaves 7e-9 either way (49
-// sequences of 88 frames, fp16: states 1.6e-6 off without it, 7.6e-7 with).  2^kRaise is 1 in 32 bits: a step of 0
+// sequences of 88 frames, fp16: states 1.6e-6 off without it, 7.3e-7 with).  2^kRaise is 1 in 32 bits: a step of 0
 // leaves the state as it was.
 constexpr float kRaise = 1.9e-8f;
 template <typename T>

@@ -5,10 +5,11 @@
 // A thread owns V channels (one 16-byte access; one channel when the rows are
 // not 16-byte aligned) and a segment of the time axis.  It keeps the last
 // taps - 1 rows in registers, so inside a segment every input is read once, and
-// has R rows on their way while it works on R others (the bound is memory).  The
-// multiply-adds go two channels at a time in packed fp32.  32 clips of up to 749
-// frames of 2048 channels in fp16 (150 MB): 34 us, 4.4 TB/s; with 128 registers
-// instead of 168, for more threads to an SM, 64 us (spills).
+// has R rows on their way while it works on R others.  The multiply-adds go two
+// channels at a time in packed fp32.  32 clips of up to 749 frames of 2048 channels:
+// fp32 56 us (298 MB, 5.3 TB/s); fp16 34.5 us (150 MB, 4.3 TB/s), where the latency
+// bounds it: the rows in flight take 168 registers, which leaves 10 warps to an SM.
+// With 128 registers it spills (64 us).
 #include <algorithm>
 
 #include "stream_ops.cuh"

@@ -423,7 +423,8 @@ def gam_ctc_collapse_noalloc(logits, lengths_dev, tokens, counts, stream=None):
 
 # ---- streaming-block operators ----
 # Their tensors are checked and passed on by the extension module _ops (csrc/python_ops.cpp).  Inference only:
-# a tensor that requires a gradient is refused while gradients are recorded.
+# a tensor that requires a gradient is refused while gradients are recorded, one with a forward-mode gradient always;
+# tensors given as outputs count as changed in place.
 
 _ops_module = None
 

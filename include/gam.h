@@ -388,7 +388,8 @@ gam_status gam_quant_linear_pack(const int8_t* q_host, int64_t n, int64_t k, uin
  * GAM_QUANT_LINEAR_MAX_ROWS (GAM_ERR_CAPACITY above), n >= 1, k a multiple of
  * 64 (GAM_ERR_SHAPE); act GAM_ACT_NONE or GAM_ACT_SWISH.  Unlike the encoder's
  * INT4 mode, which rounds q scale to fp16, neither the weights nor (in fp32) x are
- * rounded: products and sums are fp32.  What a row holds, infinities and NaN
+ * rounded.  Sums are fp32; those within a group of 64 are the tensor core's, which
+ * may truncate an addition instead of rounding it.  What a row holds, infinities and NaN
  * included, does not reach other rows, and equal calls give equal bits. */
 gam_status gam_quant_linear(const void* x_dev, int dtype, int64_t ldx, const uint8_t* packed_dev,
                             const void* scale_dev, const float* bias_dev, int act, int rows, int n, int k,
