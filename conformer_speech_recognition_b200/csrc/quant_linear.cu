@@ -796,8 +796,7 @@ gam_status launch_staged(LinearArgs p, int sms, cudaStream_t s) {
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
   if (e != cudaSuccess) return launch_status(e);
   const int smem = kRingBytes + p.rows * PARTS * (p.chunk * 128 + 16);
-  kernel<<<std::min((tiles + per_cta - 1) / per_cta, sms), kWarps * 32, smem, s>>>(p);
-  return launch_status(cudaGetLastError());
+  return launch_status(launch_kernel(kernel, std::min((tiles + per_cta - 1) / per_cta, sms), kWarps * 32, smem, s, p));
 }
 
 // Forms by size, measured in us (thin with one tile, thin with two, staged):

@@ -263,12 +263,11 @@ gam_status launch_v(const gam_residual_norm_args& p, int64_t per_gate, int sms, 
   const int vecs = (p.d + V - 1) / V + (V == 2);  // a phase can cut one pair in two
   auto warps = [&](auto kernel, int per_sm) {     // warps walk over the rows
     const int64_t groups = (p.rows + kWarps - 1) / kWarps;
-    kernel<<<(unsigned)std::min<int64_t>(groups, (int64_t)sms * per_sm), 32 * kWarps, 0, s>>>(p, per_gate);
-    return launch_status(cudaGetLastError());
+    const unsigned grid = (unsigned)std::min<int64_t>(groups, (int64_t)sms * per_sm);
+    return launch_status(launch_kernel(kernel, grid, 32 * kWarps, 0, s, p, per_gate));
   };
   auto cta = [&](auto kernel, int threads) {      // a CTA to a row; walking over them was slower
-    kernel<<<(unsigned)p.rows, threads, 0, s>>>(p, per_gate);
-    return launch_status(cudaGetLastError());
+    return launch_status(launch_kernel(kernel, (unsigned)p.rows, threads, 0, s, p, per_gate));
   };
 #define GAM_WARPS(NV, FULL, PER_SM) return warps(residual_norm_kernel<TX, TY, 32, V, NV, FULL, GATE>, PER_SM)
 #define GAM_CTA(G, NV, FULL) return cta(residual_norm_kernel<TX, TY, G, V, NV, FULL, GATE>, G)

@@ -790,10 +790,8 @@ gam_status launch_step(const gam_scan_args& p, cudaStream_t s) {
   constexpr size_t kQuad = 4 * sizeof(T);
   const bool quad = p.n % 4 == 0 && aligned(p.b, kQuad) && aligned(p.c, kQuad) && p.b_batch_stride % 4 == 0 &&
                     p.b_row_stride % 4 == 0 && p.c_batch_stride % 4 == 0 && p.c_row_stride % 4 == 0;
-  if (vec && quad) step_kernel<T, L, true, true><<<g, kStep, 0, s>>>(p);
-  else if (vec) step_kernel<T, L, true, false><<<g, kStep, 0, s>>>(p);
-  else step_kernel<T, L, false, false><<<g, kStep, 0, s>>>(p);
-  return launch_status(cudaGetLastError());
+  auto kernel = vec && quad ? step_kernel<T, L, true, true> : vec ? step_kernel<T, L, true, false> : step_kernel<T, L, false, false>;
+  return launch_status(launch_kernel(kernel, g, kStep, 0, s, p));
 }
 
 template <typename T, int S, int L, int CH>

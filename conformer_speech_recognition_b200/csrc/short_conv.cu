@@ -139,16 +139,16 @@ __global__ void __launch_bounds__(kThreads) short_conv_kernel(const ConvArgs p) 
 
 template <typename T, int V, int R>
 cudaError_t launch_taps(int taps, unsigned grid, const ConvArgs& p, cudaStream_t s) {
+  auto go = [&](auto kernel) { return launch_kernel(kernel, grid, kThreads, 0, s, p); };
   switch (taps) {
-    case 2: short_conv_kernel<T, V, 2, R><<<grid, kThreads, 0, s>>>(p); break;
-    case 3: short_conv_kernel<T, V, 3, R><<<grid, kThreads, 0, s>>>(p); break;
-    case 4: short_conv_kernel<T, V, 4, R><<<grid, kThreads, 0, s>>>(p); break;
-    case 5: short_conv_kernel<T, V, 5, R><<<grid, kThreads, 0, s>>>(p); break;
-    case 6: short_conv_kernel<T, V, 6, R><<<grid, kThreads, 0, s>>>(p); break;
-    case 7: short_conv_kernel<T, V, 7, R><<<grid, kThreads, 0, s>>>(p); break;
-    default: short_conv_kernel<T, V, 8, R><<<grid, kThreads, 0, s>>>(p); break;
+    case 2: return go(short_conv_kernel<T, V, 2, R>);
+    case 3: return go(short_conv_kernel<T, V, 3, R>);
+    case 4: return go(short_conv_kernel<T, V, 4, R>);
+    case 5: return go(short_conv_kernel<T, V, 5, R>);
+    case 6: return go(short_conv_kernel<T, V, 6, R>);
+    case 7: return go(short_conv_kernel<T, V, 7, R>);
+    default: return go(short_conv_kernel<T, V, 8, R>);
   }
-  return cudaGetLastError();
 }
 
 template <typename T>

@@ -32,6 +32,7 @@ gam_status check_device(int* sms) {
 
 gam_status launch_status(cudaError_t e) {
   if (e == cudaSuccess) return GAM_OK;
+  cudaGetLastError();  // reported here, so not to the caller's next check
   return op_fail(GAM_ERR_CUDA, std::string("launch: ") + cudaGetErrorName(e) + " (" + cudaGetErrorString(e) + ")");
 }
 

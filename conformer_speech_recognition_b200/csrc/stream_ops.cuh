@@ -8,6 +8,7 @@
 
 #include <string>
 #include <type_traits>
+#include <utility>
 
 #include "../../include/gam.h"
 #include "common.cuh"
@@ -219,8 +220,20 @@ gam_status guarded(F&& body) noexcept {
 
 // The current device is a B200 (its number of SMs in *sms); cached per device.
 gam_status check_device(int* sms);
-// Status of the launches made since the call's checks.
+// A launch's error as a status.
 gam_status launch_status(cudaError_t e);
+
+// A launch with the error of this launch alone: after <<<>>>, cudaGetLastError() also reports, and takes, what an
+// earlier call of the caller's has left.
+template <typename... P, typename... A>
+cudaError_t launch_kernel(void (*kernel)(P...), unsigned grid, int threads, size_t smem, cudaStream_t s, A&&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  return cudaLaunchKernelEx(&cfg, kernel, std::forward<A>(args)...);
+}
 
 }  // namespace ops
 }  // namespace gam

@@ -311,6 +311,30 @@ def test_norm_scale_that_requires_a_gradient_is_refused():
         gam.gam_residual_norm(x, y, alpha="half")
 
 
+def test_errors_of_other_calls_are_not_reported():
+    """An error that the caller's own CUDA call left behind is not this call's."""
+    torch = _torch()
+    cudart = ctypes.CDLL("libcudart.so.12")
+    x, y, w = torch.randn(3, 64, device="cuda"), torch.randn(3, 64, device="cuda"), torch.randn(64, 4, device="cuda")
+    t, _ = scan_inputs(40, 1, 2, 8, 4, "f32")
+    t40, _ = scan_inputs(41, 1, 40, 8, 4, "f32")
+    q = dev(gam.gam_quant_linear_pack(np.ones((131072, 128), np.int8)))
+    s = torch.ones(131072, 2, dtype=torch.float16, device="cuda")
+    xq = torch.randn(4, 128, device="cuda")
+    calls = (lambda: gam.gam_residual_norm(x, y), lambda: gam.gam_short_conv(x[None], w), lambda: scan_call(t), lambda: scan_call(t40),
+             lambda: gam.gam_quant_linear(xq, q, s), lambda: gam.gam_quant_linear(xq, q[:64], s[:64]))
+    for call in calls:
+        call()
+    torch.cuda.synchronize()
+    for call in calls:
+        assert cudart.cudaSetDevice(4096) != 0         # refused on the host, and remembered
+        try:
+            call()
+        finally:
+            cudart.cudaGetLastError()
+    torch.cuda.synchronize()
+
+
 # ---- the forms of large calls ---------------------------------------------------------
 
 @pytest.mark.parametrize("xdtype,dtype", [("f32", "f32"), ("f32", "f16"), ("bf16", "bf16")])
